@@ -31,6 +31,8 @@ __all__ = [
     "debug_stream_read", "debug_mfma_loop", "debug_decode_rate", "mfma_loop_flops", "tune", "tune_clear",
     "input_transform_swiglu", "MoeWeight", "moe_rows_max", "moe_align", "moe_input_transform", "moe_linear",
     "moe_combine", "moe_forward", "reserve_workspace", "workspace_key",
+    "Rope", "KvCache", "split_heads", "rope", "cache_write", "cache_read", "rope_cache_write", "paged_attention",
+    "prompt_attention", "attention_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -677,3 +679,9 @@ def moe_forward(x: torch.Tensor, w: MoeWeight, topk_ids: torch.Tensor, topk_weig
     xr = moe_input_transform(x, w, route, topk_ids.shape[1], block, swiglu)
     y = moe_linear(w, xr, route[1], block, x.dtype, decoder)
     return moe_combine(y, route[2], topk_weights)
+
+
+# Between the projections: rotary positions, the paged cache and attention
+# (over include/exl3_attn.h; needs the names above).
+from .attention import (KvCache, Rope, attention_workspace_bytes, cache_read, cache_write, paged_attention,  # noqa: E402
+                        prompt_attention, rope, rope_cache_write, split_heads)

@@ -1,0 +1,459 @@
+// Attention for few query rows per key/value head: one new token a sequence,
+// a handful of drafted ones, or any call too small for the large tiles.
+//
+// With S = scale * q K^T, p = exp2(S * log2(e) - m), o = (p V) / sum(p): one
+// pass over the keys with a running maximum m and sum.  A workgroup has 16
+// (or 32) query rows, the heads that share a key/value head and a few tokens,
+// as the columns of matrix products and a range of keys as the other side:
+//   S^T[key][row] = K q^T       A = 16 keys x 32 dims, B = 32 dims x 16 rows
+//   o^T[dim][row] += V^T p^T    A = 16 dims x 32 keys, B = 32 keys x 16 rows
+// Its four waves take steps of 32 keys in turn, each with its own m, sum and
+// o, and add them up at the end; nothing is shared before that, so keys and
+// values go from memory to registers without LDS.  The order of a product's
+// inner index is free, which settles the rest:
+//   - the two 16-key tiles of a step take keys {8a + b} and {8a + 4 + b}
+//     (a, b < 4), so that the scores a lane holds are those of 8 consecutive
+//     keys, exactly the lane's part of the second product's B operand: the
+//     probabilities never change lanes.
+//   - the dims of the first product follow the 16 bytes a lane loads of a
+//     key's row (8, 16 or 32 values).
+//   - a lane loads the same D/16 dims of its 8 values' rows, 16 lanes a whole
+//     row; one v_perm_b32 per pair of keys turns them into A operands whose
+//     row c is dim (D/16) * c + j for operand j.
+#pragma once
+
+#include "attn_device.hpp"
+
+namespace exl3 {
+
+constexpr int ATTN_CPOL_SC1 = 16;  // device-scope coherent access
+
+// Values a lane takes from a key's row in one load, and the loads per row
+// (four lanes share a row).
+template <int D, int BITS>
+struct KeyRun {
+  static constexpr int FIT = BITS == 4 ? 32 : BITS == 8 ? 16 : 8;  // values in 16 bytes
+  static constexpr int LEN = FIT < D / 4 ? FIT : D / 4;
+  static constexpr int LOADS = D / (4 * LEN);
+  static constexpr int WORDS = LEN * (BITS == 4 ? 4 : BITS == 8 ? 8 : 16) / 32;
+};
+
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t *a) {
+  if constexpr (WORDS == 1) {
+    w[0] = *(const uint32_t *)a;
+  } else if constexpr (WORDS == 2) {
+    const u32x2_t v = *(const u32x2_t *)a;
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const u32x4_t v = *(const u32x4_t *)(a + 16 * i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+}
+
+// 8 values as four pairs, from 16-bit values or codes; `at` counts 8s.
+template <bool BF16, int BITS, int WORDS>
+__device__ __forceinline__ u32x4_t eight(const uint32_t (&w)[WORDS], int at, float s) {
+  if constexpr (BITS == 4) {
+    const uint32_t x = w[at];
+    return (u32x4_t){Half<BF16>::template fp4<0>(x, s), Half<BF16>::template fp4<1>(x, s),
+                     Half<BF16>::template fp4<2>(x, s), Half<BF16>::template fp4<3>(x, s)};
+  } else if constexpr (BITS == 8) {
+    const uint32_t x = w[2 * at], y = w[2 * at + 1];
+    return (u32x4_t){Half<BF16>::template fp8<false>(x, s), Half<BF16>::template fp8<true>(x, s),
+                     Half<BF16>::template fp8<false>(y, s), Half<BF16>::template fp8<true>(y, s)};
+  } else {
+    return (u32x4_t){w[4 * at], w[4 * at + 1], w[4 * at + 2], w[4 * at + 3]};
+  }
+}
+
+// Whether a pair of 16-bit values has an infinity or NaN.
+template <bool BF16>
+__device__ __forceinline__ bool odd_pair(uint32_t x) {
+  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u;
+  return (x & E) == E || ((x >> 16) & E) == E;
+}
+
+// Of a pair: CLASS 0, infinities and NaN replaced by 0; 1, 2, 3: 1 where the
+// value is a NaN, +infinity, -infinity, else 0.
+template <bool BF16>
+__device__ __forceinline__ uint32_t class_pair(uint32_t x, int cls) {
+  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u, ONE = BF16 ? 0x3F80u : 0x3C00u;
+  uint32_t out = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t v = (x >> (16 * h)) & 0xFFFFu;
+    const bool odd = (v & E) == E;
+    const uint32_t kind = !odd ? 0u : (v & 0x7FFFu) > E ? 1u : (v >> 15) ? 3u : 2u;
+    const uint32_t r = cls == 0 ? (odd ? 0u : v) : (kind == (uint32_t)cls ? ONE : 0u);
+    out |= r << (16 * h);
+  }
+  return out;
+}
+
+// What rows gain from the infinities and NaN of values they see: cnt is how
+// many of the class a row sees in a dim.
+__device__ __forceinline__ float odd_value(float cnt, int cls) {
+  return cnt > 0.f ? __uint_as_float(cls == 1 ? 0x7FC00000u : cls == 2 ? 0x7F800000u : 0xFF800000u) : 0.f;
+}
+
+template <bool BF16, int D, int BITS, int NT>
+__global__ __launch_bounds__(256) void attn_small_kernel(AttnParams p) {
+  constexpr bool PAGED = BITS != 0;
+  constexpr int CB = PAGED ? BITS : 16;  // bits of a stored value
+  constexpr int R = 16 * NT;
+  constexpr int DV = D / 16;             // dims of a row that a lane holds of the second product
+  constexpr int DP = D / 32;             // as pairs
+  using KR = KeyRun<D, CB>;
+  constexpr int VW = DV * CB >= 32 ? DV * CB / 32 : 1;  // words of a lane's dims of one value row
+  __shared__ float s_o[4][64][DV + 1];
+  __shared__ float s_m[4][R], s_l[4][R];
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = lane & 15, g = lane >> 4;
+  const int head = blockIdx.x % p.heads_kv;
+  const int item = blockIdx.x / p.heads_kv;
+  Work w;
+  int C;
+  if (!find_work<R>(p, item, lane, w, C)) return;
+
+  // ---- the tile's rows and their keys
+  const int rows = w.q_len * p.group;
+  const int r0 = w.tile * R;
+  const int r_last = min(r0 + R, rows) - 1;
+  const int shift = w.kv_len - w.q_len;  // a new token's position is its index + shift
+  const int p_first = shift + r0 / p.group, p_last = shift + r_last / p.group;
+  const int hi_all = p.causal ? min(w.kv_len, p_last + 1) : w.kv_len;
+  const int lo_all = p.window > 0 ? max(0, p_first - p.window + 1) : 0;
+  const int64_t from = (int64_t)(lo_all & ~31) + (int64_t)w.split * C;
+  const int lo = (int)min<int64_t>(max<int64_t>(from, lo_all), 0x7FFFFF00);
+  const int hi = (int)min<int64_t>(from + C, hi_all);
+
+  int first[NT], span[NT];  // the keys first .. first + span - 1 are those the lane's row (column c of tile n) sees
+  const uint16_t *q_row[NT];
+  bool live[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = r0 + 16 * n + c;
+    live[n] = r < rows;
+    const int i = (live[n] ? r : r_last) / p.group;
+    const int h = (live[n] ? r : r_last) - i * p.group;
+    const int pos = shift + i;
+    first[n] = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
+    span[n] = max(0, (p.causal ? min(hi, pos + 1) : hi) - first[n]);
+    q_row[n] = p.q.data + (int64_t)(w.q0 + i) * p.q.token + (int64_t)(head * p.group + h) * p.q.head;
+  }
+  // B operands of the first product: dims in the order the key loads have
+  u32x4_t q[NT][D / 32];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) {
+      const int u = t / (KR::LEN / 8), e = t % (KR::LEN / 8);
+      q[n][t] = *(const u32x4_t *)(q_row[n] + u * 4 * KR::LEN + g * KR::LEN + 8 * e);
+    }
+
+  // ---- where keys and values lie
+  const int ps_mask = (1 << p.cache.page_shift) - 1;
+  const int32_t *table = PAGED ? p.page_table + (int64_t)w.seq * p.table_stride : nullptr;
+  // lane's keys of a step at k0: first product k0 + 8*(c/4) + c%4 and 4 more,
+  // second product k0 + 8*g .. + 7; each within one page (pages hold whole 16s)
+  auto page_of = [&](int key) __attribute__((always_inline)) -> int {
+    const int i = key >> p.cache.page_shift;
+    int pg = -1;
+    if (key < hi && i < p.table_width) pg = table[i];
+    return pg >= 0 && pg < p.cache.pages ? pg : -1;
+  };
+  uint32_t kw[2][KR::LOADS][KR::WORDS], vw[8][VW];
+  uint32_t ksc[2][2], vsc[8];  // scale bytes: of a key's row, of the lane's block of a value row
+  auto load_k = [&](int k0, int pg) __attribute__((always_inline)) {
+    const int key = k0 + 8 * (c >> 2) + (c & 3);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t *a;
+      const uint8_t *sa = nullptr;
+      if constexpr (PAGED) {
+        const int64_t r = ((int64_t)head << p.cache.page_shift) + ((key + 4 * t) & ps_mask);
+        const int pi = max(pg, 0);  // a hole reads page 0 and is masked
+        a = p.cache.k + pi * p.cache.k_page + r * (D * CB / 8);
+        if constexpr (CB < 16) sa = p.cache.k_scale + pi * p.cache.ks_page + r * (D / 32);
+      } else {
+        a = (const uint8_t *)(p.k.data + (int64_t)(w.q0 + min(key + 4 * t, hi - 1)) * p.k.token +
+                              (int64_t)head * p.k.head);
+      }
+#pragma unroll
+      for (int u = 0; u < KR::LOADS; ++u) load_words(kw[t][u], a + (u * 4 + g) * KR::LEN * CB / 8);
+      if constexpr (CB < 16) {
+        if constexpr (D == 64) ksc[t][0] = *(const uint16_t *)sa;
+        else if constexpr (D == 128) ksc[t][0] = *(const uint32_t *)sa;
+        else {
+          const u32x2_t v = *(const u32x2_t *)sa;
+          ksc[t][0] = v.x, ksc[t][1] = v.y;
+        }
+      }
+    }
+  };
+  auto load_v = [&](int k0, int pg) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int key = k0 + 8 * g + i;
+      const uint8_t *a;
+      if constexpr (PAGED) {
+        const int64_t r = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
+        const int pi = max(pg, 0);
+        a = p.cache.v + pi * p.cache.v_page + r * (D * CB / 8) + c * (DV * CB / 8);
+        if constexpr (CB < 16) vsc[i] = p.cache.v_scale[pi * p.cache.vs_page + r * (D / 32) + (c * DV) / 32];
+      } else {
+        a = (const uint8_t *)(p.v.data + (int64_t)(w.q0 + min(key, hi - 1)) * p.v.token + (int64_t)head * p.v.head +
+                              c * DV);
+      }
+      if constexpr (DV * CB < 32) vw[i][0] = *(const uint16_t *)a;
+      else load_words(vw[i], a);
+    }
+  };
+
+  float4_t o[NT][DV];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m[n] = -INFINITY;
+    l[n] = 0.f;
+#pragma unroll
+    for (int j = 0; j < DV; ++j) o[n][j] = (float4_t){0.f, 0.f, 0.f, 0.f};
+  }
+
+  int k0 = (lo & ~31) + 32 * wave;
+  int pk = 0, pv = 0;
+  if (k0 < hi) {
+    if constexpr (PAGED) {
+      pk = page_of(k0 + 8 * (c >> 2));
+      pv = page_of(k0 + 8 * g);
+    }
+    load_k(k0, pk);
+    load_v(k0, pv);
+  }
+  for (; k0 < hi; k0 += 128) {
+    int pk2 = 0, pv2 = 0;
+    const bool more = k0 + 128 < hi;
+    if constexpr (PAGED)
+      if (more) {
+        pk2 = page_of(k0 + 128 + 8 * (c >> 2));
+        pv2 = page_of(k0 + 128 + 8 * g);
+      }
+    // ---- scores
+    float4_t s[NT][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][t] = (float4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) {
+        const int u = d / (KR::LEN / 8), e = d % (KR::LEN / 8);
+        float sc = 1.f;
+        if constexpr (CB < 16) {
+          const int block = u * (4 * KR::LEN / 32) + (g * KR::LEN + 8 * e) / 32;
+          const uint32_t word = D == 256 && block >= 4 ? ksc[t][1] : ksc[t][0];
+          sc = scale_of((word >> (8 * (block & 3))) & 255u);
+        }
+        const u32x4_t a = eight<BF16, CB>(kw[t][u], e, sc);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][t] = Half<BF16>::mfma16(a, q[n][d], s[n][t]);
+      }
+    }
+    if (more) load_k(k0 + 128, pk2);
+    // ---- mask: key of score (t, i) is k0 + 8g + 4t + i
+    const bool hole = PAGED && pv < 0;
+    const bool whole = k0 >= lo && k0 + 32 <= hi && (!p.causal || k0 + 31 <= p_first) &&
+                       (p.window == 0 || k0 > p_last - p.window) && !__any(hole);
+    uint32_t seen[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      seen[n] = 255u;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][t][i] *= p.scale_log2;
+      if (!whole) {
+        seen[n] = 0u;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool ok = (uint32_t)(k0 + 8 * g + 4 * t + i - first[n]) < (hole ? 0u : (uint32_t)span[n]);
+            s[n][t][i] = ok ? s[n][t][i] : -INFINITY;
+            seen[n] |= ok ? 1u << (4 * t + i) : 0u;
+          }
+      }
+    }
+    // ---- probabilities
+    u32x4_t pr[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float top = m[n];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[n][t][i]);
+      top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
+      top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+      const float base = top == -INFINITY ? 0.f : top;
+      const float keep = __builtin_amdgcn_exp2f(m[n] - base);
+      m[n] = top;
+      float pf[8];
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pf[4 * t + i] = __builtin_amdgcn_exp2f(s[n][t][i] - base);
+          sum += pf[4 * t + i];
+        }
+      l[n] = l[n] * keep + sum;
+#pragma unroll
+      for (int j = 0; j < DV; ++j) o[n][j] *= keep;
+      // rounded to the type for the product (error 2^-9 or 2^-12 of each
+      // term, no larger than the output's own rounding); l sums them unrounded
+      pr[n] = (u32x4_t){Half<BF16>::pack(pf[0], pf[1]), Half<BF16>::pack(pf[2], pf[3]), Half<BF16>::pack(pf[4], pf[5]),
+                        Half<BF16>::pack(pf[6], pf[7])};
+    }
+    // ---- values
+    uint32_t vp[8][DP];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!whole) {  // keys outside the range or in a hole: whatever is stored there counts as zero
+        if ((uint32_t)(k0 + 8 * g + i - lo) >= (hole ? 0u : (uint32_t)(hi - lo))) {
+#pragma unroll
+          for (int x = 0; x < VW; ++x) vw[i][x] = 0u;
+          if constexpr (CB < 16) vsc[i] = 127u;
+        }
+      }
+      if constexpr (CB == 16) {
+#pragma unroll
+        for (int x = 0; x < DP; ++x) vp[i][x] = vw[i][x];
+      } else {
+        const float sc = scale_of(vsc[i]);
+        if constexpr (DV == 4) {
+          if constexpr (CB == 8) {
+            vp[i][0] = Half<BF16>::template fp8<false>(vw[i][0], sc);
+            vp[i][1] = Half<BF16>::template fp8<true>(vw[i][0], sc);
+          } else {
+            vp[i][0] = Half<BF16>::template fp4<0>(vw[i][0], sc);
+            vp[i][1] = Half<BF16>::template fp4<1>(vw[i][0], sc);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < DV / 8; ++x) {
+            const u32x4_t v = eight<BF16, CB>(vw[i], x, sc);
+            vp[i][4 * x] = v.x, vp[i][4 * x + 1] = v.y, vp[i][4 * x + 2] = v.z, vp[i][4 * x + 3] = v.w;
+          }
+        }
+      }
+    }
+    if (more) load_v(k0 + 128, pv2);
+    pk = pk2;
+    pv = pv2;
+    auto a_of = [&](int j) __attribute__((always_inline)) -> u32x4_t {
+      const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
+      u32x4_t a;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) a[x] = __builtin_amdgcn_perm(vp[2 * x + 1][j >> 1], vp[2 * x][j >> 1], sel);
+      return a;
+    };
+    bool odd = false;
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int x = 0; x < DP; ++x) odd = odd || odd_pair<BF16>(vp[i][x]);
+    }
+    if (__builtin_expect(!__any(odd), 1)) {
+#pragma unroll
+      for (int j = 0; j < DV; ++j) {
+        const u32x4_t a = a_of(j);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][j] = Half<BF16>::mfma16(a, pr[n], o[n][j]);
+      }
+    } else {
+      // An infinity or NaN among values that some rows must not see: 0 * inf
+      // would reach them through the product.  The finite values take the
+      // product; then each class of the others is counted by a product of
+      // ones with what each row sees.
+#pragma unroll
+      for (int j = 0; j < DV; ++j) {
+        const u32x4_t a = a_of(j);
+        for (int cls = 0; cls < 4; ++cls) {
+          u32x4_t x;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) x[y] = class_pair<BF16>(a[y], cls);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (cls == 0) {
+              o[n][j] = Half<BF16>::mfma16(x, pr[n], o[n][j]);
+            } else {
+              constexpr uint32_t ONE = BF16 ? 0x3F80u : 0x3C00u;
+              u32x4_t b;
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                b[y] = ((seen[n] >> (2 * y)) & 1u) * ONE | (((seen[n] >> (2 * y + 1)) & 1u) * ONE) << 16;
+              const float4_t cnt = Half<BF16>::mfma16(x, b, (float4_t){0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[n][j][i] += odd_value(cnt[i], cls);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // ---- the waves' results together: wave i sums element i of every tile
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    l[n] += __shfl_xor(l[n], 16, 64);
+    l[n] += __shfl_xor(l[n], 32, 64);
+    if (g == 0) {
+      s_m[wave][16 * n + c] = m[n];
+      s_l[wave][16 * n + c] = l[n];
+    }
+  }
+  __syncthreads();
+  const bool last_of_one = w.splits == 1;
+  float *part = p.part + (int64_t)blockIdx.x * (R * (D + 2));
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) top = __builtin_fmaxf(top, s_m[x][16 * n + c]);
+    // a NaN score leaves top as the others' maximum, and its own sum NaN
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) total += s_l[x][16 * n + c] * __builtin_amdgcn_exp2f(s_m[x][16 * n + c] - base);
+    const float keep = __builtin_amdgcn_exp2f(m[n] - base);
+    float mine[DV];
+    for (int i = 0; i < 4; ++i) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < DV; ++j) s_o[wave][lane][j] = (i == 0 ? o[n][j][0] : i == 1 ? o[n][j][1] : i == 2 ? o[n][j][2] : o[n][j][3]) * keep;
+      __syncthreads();
+      if (wave == i) {
+#pragma unroll
+        for (int j = 0; j < DV; ++j) mine[j] = (s_o[0][lane][j] + s_o[1][lane][j]) + (s_o[2][lane][j] + s_o[3][lane][j]);
+      }
+    }
+    if (live[n] && last_of_one) {
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const int r = r0 + 16 * n + c;
+      const int i = r / p.group, h = r - i * p.group;
+      uint16_t *y = p.out.data + (int64_t)(w.q0 + i) * p.out.token + (int64_t)(head * p.group + h) * p.out.head +
+                    DV * (4 * g + wave);
+#pragma unroll
+      for (int j = 0; j < DV; j += 2) *(uint32_t *)(y + j) = Half<BF16>::pack(mine[j] * inv, mine[j + 1] * inv);
+    }
+  }
+  (void)part;
+}
+
+}  // namespace exl3

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "../../include/exl3.h"
+#include "exl3_host.hpp"
 #include "exl3_launch.hpp"
 
 namespace {
@@ -1525,5 +1526,17 @@ exl3_status linear_in_scratch(const exl3_weight *w, const uint16_t *x_rot, int32
 }
 
 exl3_status scratch_setup_error(hipError_t e, const char *what) { return launch_error(e, what); }
+
+exl3_status host_fail(exl3_status s, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+  va_end(ap);
+  return s;
+}
+
+void host_clear_error() { clear_error(); }
+
+int host_cus() { return device_cus_or_default(); }
 
 }  // namespace exl3
