@@ -107,8 +107,9 @@ struct Work {
 
 // Every wave of the workgroup finds the same answer.  Sequence s has
 // tiles(s) = ceil(q_len * group / R) tiles and, when the call splits keys,
-// ceil(kv_len / C) parts of each, C the keys of a part: the keys of all
-// tiles over `target` work items, a multiple of 64 and at least 256.
+// ceil(span / C) parts of each, span the keys that a tile's rows see at most
+// and C the keys of a part: the keys of all tiles over `target` work items, a
+// multiple of 128 (a step of the four waves) and at least part_min.
 template <int R>
 __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w, int &C) {
   auto shape = [&](int s, int &q0, int &ql, int &kv, int &tiles) __attribute__((always_inline)) {
@@ -121,24 +122,28 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       tiles = (int)(((int64_t)ql * p.group + R - 1) / R);
     }
   };
-  C = 0x7FFFFFC0;
+  // a tile's rows are at most R tokens; its keys start at a multiple of 32
+  auto span = [&](int kv) __attribute__((always_inline)) {
+    return p.window > 0 ? min(kv, min(p.window, 0x3FFFFFFF) + R + 32) : kv;
+  };
+  C = 0x7FFFFF80;
   if (p.target > 0) {
     int64_t keys = 0;
     for (int s0 = 0; s0 < p.batch; s0 += 64) {
       int q0, ql, kv, tiles;
       shape(s0 + lane, q0, ql, kv, tiles);
-      keys += (int64_t)tiles * kv;
+      keys += (int64_t)tiles * span(kv);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) keys += __shfl_xor(keys, d, 64);
-    const int64_t c = ((keys + p.target - 1) / p.target + 63) & ~63ll;
-    C = (int)min<int64_t>(max<int64_t>(c, 256), 0x7FFFFFC0);
+    const int64_t c = ((keys + p.target - 1) / p.target + 127) & ~127ll;
+    C = (int)min<int64_t>(max<int64_t>(c, p.part_min), 0x7FFFFF80);
   }
   int base = 0, tbase = 0;
   for (int s0 = 0; s0 < p.batch; s0 += 64) {
     int q0, ql, kv, tiles;
     shape(s0 + lane, q0, ql, kv, tiles);
-    const int splits = max(1, (int)(((int64_t)kv + C - 1) / C));
+    const int splits = max(1, (int)(((int64_t)span(kv) + C - 1) / C));
     const int n = tiles * splits;
     const int incl = wave_inclusive_sum(n, lane);
     const int tincl = wave_inclusive_sum(tiles, lane);

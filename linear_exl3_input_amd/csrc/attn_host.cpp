@@ -162,8 +162,13 @@ exl3_status launched(hipError_t e, const char *what) {
 struct AttnPlan {
   int32_t columns;  // 16-row column tiles of a workgroup (small kernel)
   int32_t target;   // work items per head that splitting aims at; 0: keys are not split
+  int32_t part_min;
   size_t workspace;
 };
+
+// Work items that splitting the keys aims at, and the least keys of a part.
+constexpr int32_t WG_PER_CU = 2;
+constexpr int32_t PART_MIN = 256;
 
 exl3_status check_attention_sizes(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads) {
   if (batch < 0 || batch > MAX_BATCH)
@@ -181,8 +186,18 @@ exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads, int32
   const double rows = batch > 0 ? (double)tokens * group / batch : 0.0;  // a sequence's, on one key/value head
   pl->columns = rows > 16.0 && head_dim < 256 ? 2 : 1;
   pl->target = 0;
+  pl->part_min = PART_MIN;
   pl->workspace = 0;
-  const int64_t items = (int64_t)tokens * group / (16 * pl->columns) + batch + pl->target;
+  const int32_t R = 16 * pl->columns;
+  const int64_t tiles = (int64_t)tokens * group / R + batch;  // at most, on each key/value head
+  // Keys are split while the tiles alone do not fill the GPU.
+  const int64_t want = (int64_t)WG_PER_CU * exl3::host_cus();
+  if (tiles * kv_heads < want && tiles * kv_heads <= EXL3_WORKSPACE_COUNTER_BYTES / 4) {
+    pl->target = (int32_t)std::max<int64_t>(1, want / kv_heads);
+    pl->workspace = EXL3_WORKSPACE_COUNTER_BYTES +
+                    (size_t)(tiles + pl->target) * kv_heads * R * (head_dim + 2) * sizeof(float);
+  }
+  const int64_t items = tiles + pl->target;
   if (items * kv_heads > MAX_GRID)
     return host_fail(EXL3_ERR_UNSUPPORTED, "%d tokens x %d heads: more tiles than a launch holds", tokens, q_heads);
   return EXL3_OK;
@@ -202,6 +217,7 @@ exl3_status run_attention(exl3::AttnParams &p, int32_t head_dim, bool bf16, int3
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + EXL3_WORKSPACE_COUNTER_BYTES);
   }
   p.target = pl.target;
+  p.part_min = pl.part_min;
   return launched(exl3::launch_attn_small(head_dim, bf16, bits, p, pl.columns, s), "attention launch");
 }
 

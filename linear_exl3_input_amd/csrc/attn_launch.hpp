@@ -56,6 +56,7 @@ struct AttnParams {
   uint32_t *counters;         // workspace: arrivals of the split tiles
   float *part;                // workspace: partial results of the split tiles
   int32_t target;             // work items per head aimed at when keys are split (0: not split)
+  int32_t part_min;           // least keys of a part, a multiple of 128
 };
 
 // bits: 0 (no cache), 16, 8, 4.

@@ -100,8 +100,26 @@ __device__ __forceinline__ float odd_value(float cnt, int cls) {
   return cnt > 0.f ? __uint_as_float(cls == 1 ? 0x7FC00000u : cls == 2 ? 0x7F800000u : 0xFF800000u) : 0.f;
 }
 
+// N consecutive dims, from d on, of row r of the tile's sequence.
+template <bool BF16, int N>
+__device__ __forceinline__ void store_row(const AttnParams &p, const Work &w, int r, int head, int d,
+                                          const float (&v)[N], float total) {
+  const float inv = total == 0.f ? 0.f : 1.f / total;  // a row that sees no key is zero
+  const int i = r / p.group, h = r - i * p.group;
+  uint16_t *y = p.out.data + (int64_t)(w.q0 + i) * p.out.token + (int64_t)(head * p.group + h) * p.out.head + d;
+  uint32_t x[N / 2];
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) x[j] = Half<BF16>::pack(v[2 * j] * inv, v[2 * j + 1] * inv);
+  if constexpr (N == 4) {
+    *(u32x2_t *)y = (u32x2_t){x[0], x[1]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < N / 2; j += 4) *(u32x4_t *)(y + 2 * j) = (u32x4_t){x[j], x[j + 1], x[j + 2], x[j + 3]};
+  }
+}
+
 template <bool BF16, int D, int BITS, int NT>
-__global__ __launch_bounds__(256) void attn_small_kernel(AttnParams p) {
+__global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(AttnParams p) {
   constexpr bool PAGED = BITS != 0;
   constexpr int CB = PAGED ? BITS : 16;  // bits of a stored value
   constexpr int R = 16 * NT;
@@ -419,8 +437,13 @@ __global__ __launch_bounds__(256) void attn_small_kernel(AttnParams p) {
     }
   }
   __syncthreads();
-  const bool last_of_one = w.splits == 1;
-  float *part = p.part + (int64_t)blockIdx.x * (R * (D + 2));
+  // A tile whose keys are split writes its part to the workspace; the last of
+  // the tile's workgroups to arrive adds the parts up in their order, so the
+  // result does not depend on which one that is.
+  constexpr int PART = R * (D + 2);  // o as [n][wave][lane][DV], then m and the sum of each row
+  const bool split = w.splits > 1;
+  __amdgpu_buffer_rsrc_t rs;
+  if (split) rs = __builtin_amdgcn_make_buffer_rsrc(p.part + (int64_t)blockIdx.x * PART, (short)0, PART * 4, 0x00020000);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float top = -INFINITY;
@@ -436,24 +459,85 @@ __global__ __launch_bounds__(256) void attn_small_kernel(AttnParams p) {
     for (int i = 0; i < 4; ++i) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < DV; ++j) s_o[wave][lane][j] = (i == 0 ? o[n][j][0] : i == 1 ? o[n][j][1] : i == 2 ? o[n][j][2] : o[n][j][3]) * keep;
+      for (int j = 0; j < DV; ++j)
+        s_o[wave][lane][j] = (i == 0 ? o[n][j][0] : i == 1 ? o[n][j][1] : i == 2 ? o[n][j][2] : o[n][j][3]) * keep;
       __syncthreads();
       if (wave == i) {
 #pragma unroll
         for (int j = 0; j < DV; ++j) mine[j] = (s_o[0][lane][j] + s_o[1][lane][j]) + (s_o[2][lane][j] + s_o[3][lane][j]);
       }
     }
-    if (live[n] && last_of_one) {
-      const float inv = total == 0.f ? 0.f : 1.f / total;
-      const int r = r0 + 16 * n + c;
-      const int i = r / p.group, h = r - i * p.group;
-      uint16_t *y = p.out.data + (int64_t)(w.q0 + i) * p.out.token + (int64_t)(head * p.group + h) * p.out.head +
-                    DV * (4 * g + wave);
+    if (split) {
 #pragma unroll
-      for (int j = 0; j < DV; j += 2) *(uint32_t *)(y + j) = Half<BF16>::pack(mine[j] * inv, mine[j + 1] * inv);
+      for (int j = 0; j < DV; j += 4)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, (float4_t){mine[j], mine[j + 1], mine[j + 2], mine[j + 3]}),
+                                               rs, (((n * 4 + wave) * 64 + lane) * DV + j) * 4, 0, ATTN_CPOL_SC1);
+      if (wave == 0 && g == 0) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), rs, (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(total), rs, (R * D + R + 16 * n + c) * 4, 0, ATTN_CPOL_SC1);
+      }
+    } else if (live[n]) {
+      store_row<BF16, DV>(p, w, r0 + 16 * n + c, head, DV * (4 * g + wave), mine, total);
     }
   }
-  (void)part;
+  if (!split) return;
+
+  __shared__ int s_last;
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // the wave's stores have been made (vmcnt 0)
+  __syncthreads();
+  uint32_t *counter = p.counters + w.slot * p.heads_kv + head;
+  if (threadIdx.x == 0)
+    s_last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)w.splits - 1u;
+  __syncthreads();
+  if (!s_last) return;
+  // parts of one tile and head lie heads_kv apart
+  float *first_part = p.part + ((int64_t)blockIdx.x - (int64_t)w.split * p.heads_kv) * PART;
+  const int64_t stride = (int64_t)p.heads_kv * PART;
+  constexpr int U = D == 256 ? 4 : 8;  // parts in flight
+  auto part_of = [&](int x) __attribute__((always_inline)) {
+    return __builtin_amdgcn_make_buffer_rsrc(first_part + x * stride, (short)0, PART * 4, 0x00020000);
+  };
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float top = -INFINITY;
+    for (int x0 = 0; x0 < w.splits; x0 += 2 * U) {
+      float mx[2 * U];
+#pragma unroll
+      for (int x = 0; x < 2 * U; ++x)
+        mx[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_of(min(x0 + x, w.splits - 1)),
+                                                                     (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
+#pragma unroll
+      for (int x = 0; x < 2 * U; ++x) top = __builtin_fmaxf(top, mx[x]);
+    }
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f, acc[DV];
+#pragma unroll
+    for (int j = 0; j < DV; ++j) acc[j] = 0.f;
+    for (int x0 = 0; x0 < w.splits; x0 += U) {
+      float mx[U], lx[U];
+      float4_t ox[U][DV / 4];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const auto r = part_of(min(x0 + x, w.splits - 1));
+        mx[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
+        lx[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (R * D + R + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
+#pragma unroll
+        for (int j = 0; j < DV / 4; ++j)
+          ox[x][j] = __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                      r, (((n * 4 + wave) * 64 + lane) * DV + 4 * j) * 4, 0, ATTN_CPOL_SC1));
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x)
+        if (x0 + x < w.splits) {
+          const float f = __builtin_amdgcn_exp2f(mx[x] - base);
+          total += lx[x] * f;
+#pragma unroll
+          for (int j = 0; j < DV; ++j) acc[j] += ox[x][j / 4][j % 4] * f;
+        }
+    }
+    if (live[n]) store_row<BF16, DV>(p, w, r0 + 16 * n + c, head, DV * (4 * g + wave), acc, total);
+  }
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 }  // namespace exl3
