@@ -160,7 +160,7 @@ exl3_status launched(hipError_t e, const char *what) {
 // ------------------------------------------------------------ attention
 
 struct AttnPlan {
-  int32_t columns;  // 16-row column tiles of a workgroup (small kernel)
+  int32_t columns;  // 16-row column tiles of a workgroup of the small kernel; 0: the tile kernel
   int32_t target;   // work items per head that splitting aims at; 0: keys are not split
   int32_t part_min;
   size_t workspace;
@@ -169,6 +169,8 @@ struct AttnPlan {
 // Work items that splitting the keys aims at, and the least keys of a part.
 constexpr int32_t WG_PER_CU = 2;
 constexpr int32_t PART_MIN = 256;
+// A sequence's rows on one key/value head from which the tile kernel runs.
+constexpr double TILE_MIN_ROWS = 48.0;
 
 exl3_status check_attention_sizes(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads) {
   if (batch < 0 || batch > MAX_BATCH)
@@ -184,11 +186,11 @@ exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads, int32
                            AttnPlan *pl) {
   const int32_t group = q_heads / kv_heads;
   const double rows = batch > 0 ? (double)tokens * group / batch : 0.0;  // a sequence's, on one key/value head
-  pl->columns = rows > 16.0 && head_dim < 256 ? 2 : 1;
+  pl->columns = rows > TILE_MIN_ROWS ? 0 : rows > 16.0 && head_dim < 256 ? 2 : 1;
   pl->target = 0;
   pl->part_min = PART_MIN;
   pl->workspace = 0;
-  const int32_t R = 16 * pl->columns;
+  const int32_t R = pl->columns > 0 ? 16 * pl->columns : exl3::ATTN_TILE_ROWS;
   const int64_t tiles = (int64_t)tokens * group / R + batch;  // at most, on each key/value head
   // Keys are split while the tiles alone do not fill the GPU.
   const int64_t want = (int64_t)WG_PER_CU * exl3::host_cus();
@@ -218,7 +220,9 @@ exl3_status run_attention(exl3::AttnParams &p, int32_t head_dim, bool bf16, int3
   }
   p.target = pl.target;
   p.part_min = pl.part_min;
-  return launched(exl3::launch_attn_small(head_dim, bf16, bits, p, pl.columns, s), "attention launch");
+  const hipError_t e = pl.columns > 0 ? exl3::launch_attn_small(head_dim, bf16, bits, p, pl.columns, s)
+                                      : exl3::launch_attn_tile(head_dim, bf16, bits, p, s);
+  return launched(e, "attention launch");
 }
 
 exl3_status check_scale(float scale) {
@@ -241,6 +245,16 @@ hipError_t launch_attn_small(int head_dim, bool bf16, int bits, const AttnParams
   return head_dim == 64    ? launch_attn_small_d64(bf16, bits, p, columns, s)
          : head_dim == 128 ? launch_attn_small_d128(bf16, bits, p, columns, s)
                            : launch_attn_small_d256(bf16, bits, p, columns, s);
+}
+
+hipError_t launch_attn_tile_d64(bool bf16, int bits, const AttnParams &p, hipStream_t s);
+hipError_t launch_attn_tile_d128(bool bf16, int bits, const AttnParams &p, hipStream_t s);
+hipError_t launch_attn_tile_d256(bool bf16, int bits, const AttnParams &p, hipStream_t s);
+
+hipError_t launch_attn_tile(int head_dim, bool bf16, int bits, const AttnParams &p, hipStream_t s) {
+  return head_dim == 64    ? launch_attn_tile_d64(bf16, bits, p, s)
+         : head_dim == 128 ? launch_attn_tile_d128(bf16, bits, p, s)
+                           : launch_attn_tile_d256(bf16, bits, p, s);
 }
 
 }  // namespace exl3

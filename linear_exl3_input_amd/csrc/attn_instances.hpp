@@ -1,6 +1,6 @@
 // Instances of the attention kernels for one head size (EXL3_HEAD_DIM) and
 // their launchers; included by one source file per size.
-#include "attn_small.hpp"
+#include "attn_tile.hpp"
 
 namespace exl3 {
 
@@ -29,6 +29,23 @@ hipError_t small_bits(int bits, const AttnParams &p, hipStream_t s) {
   }
 }
 
+template <bool BF16, int BITS>
+hipError_t tile_of(const AttnParams &p, hipStream_t s) {
+  const dim3 grid((unsigned)(grid_items(p, TileGeom<EXL3_HEAD_DIM>::ROWS) * p.heads_kv));
+  hipLaunchKernelGGL((attn_tile_kernel<BF16, EXL3_HEAD_DIM, BITS>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t tile_bits(int bits, const AttnParams &p, hipStream_t s) {
+  switch (bits) {
+    case 0: return tile_of<BF16, 0>(p, s);
+    case 4: return tile_of<BF16, 4>(p, s);
+    case 8: return tile_of<BF16, 8>(p, s);
+    default: return tile_of<BF16, 16>(p, s);
+  }
+}
+
 }  // namespace
 
 #define EXL3_JOIN2(a, b) a##b
@@ -40,6 +57,10 @@ hipError_t EXL3_JOIN(launch_attn_small_d, EXL3_HEAD_DIM)(bool bf16, int bits, co
 #endif
   if (columns != 1) return hipErrorInvalidValue;
   return bf16 ? small_bits<true, 1>(bits, p, s) : small_bits<false, 1>(bits, p, s);
+}
+
+hipError_t EXL3_JOIN(launch_attn_tile_d, EXL3_HEAD_DIM)(bool bf16, int bits, const AttnParams &p, hipStream_t s) {
+  return bf16 ? tile_bits<true>(bits, p, s) : tile_bits<false>(bits, p, s);
 }
 
 }  // namespace exl3

@@ -66,5 +66,8 @@ hipError_t launch_cache_read(int head_dim, bool bf16, int bits, const ReadParams
 // Tiles of 16 * columns query rows, one workgroup each (columns 1 or 2).
 // bits 0: packed rows.
 hipError_t launch_attn_small(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+// Tiles of ATTN_TILE_ROWS query rows.
+constexpr int ATTN_TILE_ROWS = 128;
+hipError_t launch_attn_tile(int head_dim, bool bf16, int bits, const AttnParams &p, hipStream_t s);
 
 }  // namespace exl3
