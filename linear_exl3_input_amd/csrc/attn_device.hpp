@@ -84,13 +84,28 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 
 // ----------------------------------------------------------------- work
 
-__device__ __forceinline__ int wave_inclusive_sum(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int t = __shfl_up(v, d, 64);
-    if (lane >= d) v += t;
-  }
+// Inclusive sums over the wave's lanes by DPP moves: within rows of 16 lanes,
+// then row 0's total to row 1, 2's to 3, and the first half's to the second.
+__device__ __forceinline__ int wave_inclusive_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);  // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
   return v;
+}
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_inclusive_sum(v), 63); }
+__device__ __forceinline__ float wave_sum(float v) {
+  auto add = [&](int moved) __attribute__((always_inline)) { v += __builtin_bit_cast(float, moved); };
+  auto bits = [&]() __attribute__((always_inline)) { return __builtin_bit_cast(int, v); };
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x111, 0xF, 0xF, true));
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x112, 0xF, 0xF, true));
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x114, 0xF, 0xF, true));
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x118, 0xF, 0xF, true));
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x142, 0xA, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x143, 0xC, 0xF, false));
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits(), 63));
 }
 
 // One workgroup's work: rows [tile * R, ...) of a sequence's q_len * group
@@ -99,73 +114,160 @@ __device__ __forceinline__ int wave_inclusive_sum(int v, int lane) {
 // one tile's rows.
 struct Work {
   int seq, tile;
-  int split, splits;   // this part of the tile's keys, of how many
-  int q0, q_len;       // the sequence's first query row and their number
+  int split, splits;  // this part of the tile's keys, of how many
+  int part_keys;      // keys of a part (splits > 1)
+  int q0, q_len;      // the sequence's first query row and their number
   int kv_len;
-  int slot;            // the tile's number over all sequences
+  int part;           // splits > 1: the part's number among those of all split tiles
 };
 
 // Every wave of the workgroup finds the same answer.  Sequence s has
-// tiles(s) = ceil(q_len * group / R) tiles and, when the call splits keys,
-// ceil(span / C) parts of each, span the keys that a tile's rows see at most
-// and C the keys of a part: the keys of all tiles over `target` work items, a
-// multiple of 128 (a step of the four waves) and at least part_min.
+// tiles(s) = ceil(q_len * group / R) tiles.  When the call splits keys, those
+// of a sequence whose span (the keys that a tile's rows see at most) exceeds C
+// are split into ceil(span / C) equal parts.  C starts as the keys of all
+// tiles over `target` and grows twice by what the work items then are over
+// `target`, so that they end up near it (whole rounds of the GPU) but for
+// lengths that rounding up hits hard; it is at least part_min.  There are
+// never more than tiles + target items, nor 2 * target parts.
 template <int R>
-__device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w, int &C) {
-  auto shape = [&](int s, int &q0, int &ql, int &kv, int &tiles) __attribute__((always_inline)) {
-    q0 = ql = kv = tiles = 0;
+__device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w) {
+  struct Seq {
+    int q0, ql, kv, tiles, span;
+  };
+  auto load = [&](int s) __attribute__((always_inline)) -> Seq {
+    Seq x = {0, 0, 0, 0, 0};
     if (s < p.batch) {
       const int a = min(max(p.cu[s], 0), p.tokens), b = min(max(p.cu[s + 1], 0), p.tokens);
-      q0 = a;
-      ql = max(0, b - a);
-      kv = p.kv_len ? max(0, p.kv_len[s]) : ql;
-      tiles = (int)(((int64_t)ql * p.group + R - 1) / R);
+      x.q0 = a;
+      x.ql = max(0, b - a);
+      x.kv = p.kv_len ? max(0, p.kv_len[s]) : x.ql;
+      x.tiles = (int)(((int64_t)x.ql * p.group + R - 1) / R);
+      // a tile's rows are at most R tokens; its keys start at a multiple of 32
+      x.span = p.window > 0 ? min(x.kv, min(p.window, 0x3FFFFFFF) + R + 32) : x.kv;
     }
+    return x;
   };
-  // a tile's rows are at most R tokens; its keys start at a multiple of 32
-  auto span = [&](int kv) __attribute__((always_inline)) {
-    return p.window > 0 ? min(kv, min(p.window, 0x3FFFFFFF) + R + 32) : kv;
+  const Seq head = load(lane);  // the first 64 sequences, mostly all of them
+  auto seq_at = [&](int s0) __attribute__((always_inline)) { return s0 == 0 ? head : load(s0 + lane); };
+  int C = 0x7FFFFFFF;
+  auto splits_of = [&](const Seq &x) __attribute__((always_inline)) -> int {
+    return x.span > C ? (int)(((int64_t)x.span + C - 1) / C) : 1;
   };
-  C = 0x7FFFFF80;
   if (p.target > 0) {
-    int64_t keys = 0;
+    // in floats, whose rounding the last factor more than covers: C is never
+    // less than keys / target
+    float keys = 0.f;
     for (int s0 = 0; s0 < p.batch; s0 += 64) {
-      int q0, ql, kv, tiles;
-      shape(s0 + lane, q0, ql, kv, tiles);
-      keys += (int64_t)tiles * span(kv);
+      const Seq x = seq_at(s0);
+      keys += wave_sum((float)x.tiles * (float)x.span);
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) keys += __shfl_xor(keys, d, 64);
-    const int64_t c = ((keys + p.target - 1) / p.target + 127) & ~127ll;
-    C = (int)min<int64_t>(max<int64_t>(c, p.part_min), 0x7FFFFF80);
+    float c = __builtin_fmaxf(keys / (float)p.target * 1.0001f + 1.f, (float)p.part_min);
+    for (int i = 0; i < 2; ++i) {
+      C = (int)__builtin_fminf(c, 2147483520.f);
+      int items = 0;
+      for (int s0 = 0; s0 < p.batch; s0 += 64) {
+        const Seq x = seq_at(s0);
+        items += wave_sum(x.tiles * splits_of(x));
+      }
+      if (items <= p.target) break;
+      c = c * ((float)items / (float)p.target) + 1.f;
+    }
+    C = (int)__builtin_fminf(c, 2147483520.f);
   }
-  int base = 0, tbase = 0;
+  int base = 0, pbase = 0;
   for (int s0 = 0; s0 < p.batch; s0 += 64) {
-    int q0, ql, kv, tiles;
-    shape(s0 + lane, q0, ql, kv, tiles);
-    const int splits = max(1, (int)(((int64_t)span(kv) + C - 1) / C));
-    const int n = tiles * splits;
-    const int incl = wave_inclusive_sum(n, lane);
-    const int tincl = wave_inclusive_sum(tiles, lane);
+    const Seq x = seq_at(s0);
+    const int splits = splits_of(x);
+    const int n = x.tiles * splits, parts = splits > 1 ? n : 0;
+    const int incl = wave_inclusive_sum(n), pincl = wave_inclusive_sum(parts);
     const uint64_t past = __ballot(item < base + incl);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
-      const int excl = base + __shfl(incl - n, l, 64);
       w.seq = s0 + l;
-      w.splits = __shfl(splits, l, 64);
-      const int at = item - excl;
+      w.splits = __builtin_amdgcn_readlane(splits, l);
+      const int at = item - base - __builtin_amdgcn_readlane(incl - n, l);
       w.tile = at / w.splits;
       w.split = at - w.tile * w.splits;
-      w.q0 = __shfl(q0, l, 64);
-      w.q_len = __shfl(ql, l, 64);
-      w.kv_len = __shfl(kv, l, 64);
-      w.slot = tbase + __shfl(tincl - tiles, l, 64) + w.tile;
+      w.part_keys = ((__builtin_amdgcn_readlane(x.span, l) + w.splits - 1) / w.splits + 127) & ~127;
+      w.q0 = __builtin_amdgcn_readlane(x.q0, l);
+      w.q_len = __builtin_amdgcn_readlane(x.ql, l);
+      w.kv_len = __builtin_amdgcn_readlane(x.kv, l);
+      w.part = w.splits > 1 ? pbase + __builtin_amdgcn_readlane(pincl - parts, l) + at : 0;
       return true;
     }
-    base += __shfl(incl, 63, 64);
-    tbase += __shfl(tincl, 63, 64);
+    base += __builtin_amdgcn_readlane(incl, 63);
+    pbase += __builtin_amdgcn_readlane(pincl, 63);
   }
   return false;
+}
+
+// The keys that a workgroup reads, [lo, hi), of those the tile's rows r0 ..
+// r_last see, and the multiple of 32 where it starts.
+struct KeyRange {
+  int shift;            // a new token's position is its index + shift
+  int p_first, p_last;  // positions of the first and the last row
+  int start, lo, hi;
+};
+
+__device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w, int r0, int r_last) {
+  KeyRange k;
+  k.shift = w.kv_len - w.q_len;
+  k.p_first = k.shift + r0 / p.group;
+  k.p_last = k.shift + r_last / p.group;
+  k.hi = p.causal ? min(w.kv_len, k.p_last + 1) : w.kv_len;
+  k.lo = p.window > 0 ? max(0, k.p_first - p.window + 1) : 0;
+  if (w.splits > 1) {
+    const int64_t from = (int64_t)(k.lo & ~31) + (int64_t)w.split * w.part_keys;
+    k.lo = (int)min<int64_t>(max<int64_t>(from, k.lo), 0x7FFFFF00);
+    k.hi = (int)min<int64_t>(from + w.part_keys, k.hi);
+  }
+  k.start = k.lo & ~31;
+  return k;
+}
+
+// ------------------------------------------------- parts of a split tile
+//
+// The parts of a tile are added up in a tree of two levels, so that no
+// workgroup reads more than a few of them after another: the last of eight
+// neighbouring parts' workgroups to arrive adds those eight, in their order,
+// and the last of the eights' adds the sums.  Which workgroup does it depends
+// on timing, the order of the sum does not.  Parts are written and read with
+// device-scope accesses (the workgroups may be on different XCDs); counters
+// are zero before and after a call.
+constexpr int PART_FAN = 8;
+constexpr int ATTN_CPOL_SC1 = 16;  // device-scope coherent access
+
+// The workgroup's stores are made; true in the last of `arrivals` workgroups.
+__device__ __forceinline__ bool arrive_last_of(uint32_t *counter, int arrivals) {
+  __shared__ int s_last;
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0: the wave's stores have been made
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t n = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = n == (uint32_t)arrivals - 1u;
+    if (s_last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return s_last != 0;
+}
+
+// After the workgroup has written its part: true in the one workgroup that
+// then holds the tile's sum.  add(x0, n, step): the sum of the n parts x0,
+// x0 + step, ...; put(x): writes the sum as part x.  Each eight's counter is
+// its first part's; the tile's is part 1's, which is no eight's first.
+template <class Add, class Put>
+__device__ __forceinline__ bool add_parts(const AttnParams &p, const Work &w, int head, Add add, Put put) {
+  uint32_t *counters = p.counters + (w.part - w.split) * p.heads_kv + head;
+  const int x0 = w.split / PART_FAN * PART_FAN;
+  const int n = min(PART_FAN, w.splits - x0);
+  if (!arrive_last_of(counters + x0 * p.heads_kv, n)) return false;
+  add(x0, n, 1);
+  if (w.splits <= PART_FAN) return true;
+  put(x0);
+  const int eights = (w.splits + PART_FAN - 1) / PART_FAN;
+  if (!arrive_last_of(counters + p.heads_kv, eights)) return false;
+  add(0, eights, PART_FAN);
+  return true;
 }
 
 }  // namespace exl3

@@ -166,11 +166,16 @@ struct AttnPlan {
   size_t workspace;
 };
 
-// Work items that splitting the keys aims at, and the least keys of a part.
-constexpr int32_t WG_PER_CU = 2;
-constexpr int32_t PART_MIN = 256;
+// Splitting aims at whole rounds of the workgroups that the GPU holds at once
+// (find_work).  Few tiles split into equal parts, and one round is best (3
+// sequences of up to 120000 keys, 4 bits, heads of 256: 96 us in one round,
+// 111 in two, 136 in four); tiles of unequal keys need more, smaller parts to
+// even out (64 sequences of up to 16000 keys, 8 bits: 242 us in one round, 190
+// in two, 201 in four; chunks of up to 1000 tokens over 20000 keys on the tile
+// kernel: 890, 803 and 712 us in one, two and four).
+constexpr int32_t PART_MIN = 256;  // least keys of a part
 // A sequence's rows on one key/value head from which the tile kernel runs.
-constexpr double TILE_MIN_ROWS = 48.0;
+constexpr double TILE_MIN_ROWS = 64.0;
 
 exl3_status check_attention_sizes(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads) {
   if (batch < 0 || batch > MAX_BATCH)
@@ -186,18 +191,21 @@ exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads, int32
                            AttnPlan *pl) {
   const int32_t group = q_heads / kv_heads;
   const double rows = batch > 0 ? (double)tokens * group / batch : 0.0;  // a sequence's, on one key/value head
-  pl->columns = rows > TILE_MIN_ROWS ? 0 : rows > 16.0 && head_dim < 256 ? 2 : 1;
+  pl->columns = rows > TILE_MIN_ROWS ? 0 : rows > 32.0 && head_dim == 64 ? 4 : rows > 16.0 && head_dim < 256 ? 2 : 1;
   pl->target = 0;
   pl->part_min = PART_MIN;
   pl->workspace = 0;
-  const int32_t R = pl->columns > 0 ? 16 * pl->columns : exl3::ATTN_TILE_ROWS;
+  const bool tile = pl->columns == 0;
+  const int32_t R = tile ? exl3::ATTN_TILE_ROWS : 16 * pl->columns;
   const int64_t tiles = (int64_t)tokens * group / R + batch;  // at most, on each key/value head
-  // Keys are split while the tiles alone do not fill the GPU.
-  const int64_t want = (int64_t)WG_PER_CU * exl3::host_cus();
-  if (tiles * kv_heads < want && tiles * kv_heads <= EXL3_WORKSPACE_COUNTER_BYTES / 4) {
-    pl->target = (int32_t)std::max<int64_t>(1, want / kv_heads);
-    pl->workspace = EXL3_WORKSPACE_COUNTER_BYTES +
-                    (size_t)(tiles + pl->target) * kv_heads * R * (head_dim + 2) * sizeof(float);
+  const int64_t per_cu = (tile ? head_dim == 256 : head_dim * pl->columns >= 256) ? 1 : 2;  // workgroups, by registers
+  const int64_t round = per_cu * exl3::host_cus();
+  const int64_t rounds = 4 * tiles * kv_heads <= round ? 1 : tile ? 4 : 2;
+  const int64_t want = std::max<int64_t>(kv_heads, rounds * round);
+  if (tiles * kv_heads < want) {
+    pl->target = (int32_t)(want / kv_heads);
+    pl->workspace = EXL3_WORKSPACE_COUNTER_BYTES + (size_t)std::min(2 * (int64_t)pl->target, pl->target + tiles) *
+                                                       kv_heads * R * (head_dim + 2) * sizeof(float);
   }
   const int64_t items = tiles + pl->target;
   if (items * kv_heads > MAX_GRID)

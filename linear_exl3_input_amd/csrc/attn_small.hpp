@@ -22,11 +22,11 @@
 //     row c is dim (D/16) * c + j for operand j.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_device.hpp"
 
 namespace exl3 {
-
-constexpr int ATTN_CPOL_SC1 = 16;  // device-scope coherent access
 
 // Values a lane takes from a key's row in one load, and the loads per row
 // (four lanes share a row).
@@ -70,6 +70,24 @@ __device__ __forceinline__ u32x4_t eight(const uint32_t (&w)[WORDS], int at, flo
   }
 }
 
+// Pair x of a row's values.
+template <bool BF16, int BITS, int WORDS>
+__device__ __forceinline__ uint32_t pair_at(const uint32_t (&w)[WORDS], int x, float s) {
+  if constexpr (BITS == 4) {
+    const uint32_t v = w[x >> 2];
+    switch (x & 3) {
+      case 0: return Half<BF16>::template fp4<0>(v, s);
+      case 1: return Half<BF16>::template fp4<1>(v, s);
+      case 2: return Half<BF16>::template fp4<2>(v, s);
+      default: return Half<BF16>::template fp4<3>(v, s);
+    }
+  } else if constexpr (BITS == 8) {
+    return x & 1 ? Half<BF16>::template fp8<true>(w[x >> 1], s) : Half<BF16>::template fp8<false>(w[x >> 1], s);
+  } else {
+    return w[x];
+  }
+}
+
 // Whether a pair of 16-bit values has an infinity or NaN.
 template <bool BF16>
 __device__ __forceinline__ bool odd_pair(uint32_t x) {
@@ -77,27 +95,13 @@ __device__ __forceinline__ bool odd_pair(uint32_t x) {
   return (x & E) == E || ((x >> 16) & E) == E;
 }
 
-// Of a pair: CLASS 0, infinities and NaN replaced by 0; 1, 2, 3: 1 where the
-// value is a NaN, +infinity, -infinity, else 0.
+// A pair of 16-bit values with infinities and NaN replaced by 0.
 template <bool BF16>
-__device__ __forceinline__ uint32_t class_pair(uint32_t x, int cls) {
-  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u, ONE = BF16 ? 0x3F80u : 0x3C00u;
-  uint32_t out = 0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t v = (x >> (16 * h)) & 0xFFFFu;
-    const bool odd = (v & E) == E;
-    const uint32_t kind = !odd ? 0u : (v & 0x7FFFu) > E ? 1u : (v >> 15) ? 3u : 2u;
-    const uint32_t r = cls == 0 ? (odd ? 0u : v) : (kind == (uint32_t)cls ? ONE : 0u);
-    out |= r << (16 * h);
-  }
-  return out;
-}
-
-// What rows gain from the infinities and NaN of values they see: cnt is how
-// many of the class a row sees in a dim.
-__device__ __forceinline__ float odd_value(float cnt, int cls) {
-  return cnt > 0.f ? __uint_as_float(cls == 1 ? 0x7FC00000u : cls == 2 ? 0x7F800000u : 0xFF800000u) : 0.f;
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
+  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u;
+  if ((x & E) == E) x &= 0xFFFF0000u;
+  if (((x >> 16) & E) == E) x &= 0xFFFFu;
+  return x;
 }
 
 // N consecutive dims, from d on, of row r of the tile's sequence.
@@ -135,20 +139,14 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   const int head = blockIdx.x % p.heads_kv;
   const int item = blockIdx.x / p.heads_kv;
   Work w;
-  int C;
-  if (!find_work<R>(p, item, lane, w, C)) return;
+  if (!find_work<R>(p, item, lane, w)) return;
 
   // ---- the tile's rows and their keys
   const int rows = w.q_len * p.group;
   const int r0 = w.tile * R;
   const int r_last = min(r0 + R, rows) - 1;
-  const int shift = w.kv_len - w.q_len;  // a new token's position is its index + shift
-  const int p_first = shift + r0 / p.group, p_last = shift + r_last / p.group;
-  const int hi_all = p.causal ? min(w.kv_len, p_last + 1) : w.kv_len;
-  const int lo_all = p.window > 0 ? max(0, p_first - p.window + 1) : 0;
-  const int64_t from = (int64_t)(lo_all & ~31) + (int64_t)w.split * C;
-  const int lo = (int)min<int64_t>(max<int64_t>(from, lo_all), 0x7FFFFF00);
-  const int hi = (int)min<int64_t>(from + C, hi_all);
+  const KeyRange kr = key_range(p, w, r0, r_last);
+  const int lo = kr.lo, hi = kr.hi, p_first = kr.p_first, p_last = kr.p_last, shift = kr.shift;
 
   int first[NT], span[NT];  // the keys first .. first + span - 1 are those the lane's row (column c of tile n) sees
   const uint16_t *q_row[NT];
@@ -233,6 +231,11 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     }
   };
 
+  // whether every row sees every key of the step at k (holes aside)
+  auto whole_step = [&](int k) __attribute__((always_inline)) {
+    return k >= lo && k + 32 <= hi && (!p.causal || k + 31 <= p_first) && (p.window == 0 || k > p_last - p.window);
+  };
+
   float4_t o[NT][DV];
   float m[NT], l[NT];
 #pragma unroll
@@ -243,24 +246,28 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     for (int j = 0; j < DV; ++j) o[n][j] = (float4_t){0.f, 0.f, 0.f, 0.f};
   }
 
-  int k0 = (lo & ~31) + 32 * wave;
-  int pk = 0, pv = 0;
+  // Pages are looked up two steps ahead: loads complete in order, so a step's
+  // rows must not wait for a page number issued after the step before's rows.
+  int k0 = kr.start + 32 * wave;
+  int pk = 0, pv = 0, pk2 = 0, pv2 = 0;  // pages of this step's and the next step's keys and values
   if (k0 < hi) {
     if constexpr (PAGED) {
       pk = page_of(k0 + 8 * (c >> 2));
       pv = page_of(k0 + 8 * g);
+      pk2 = page_of(k0 + 128 + 8 * (c >> 2));
+      pv2 = page_of(k0 + 128 + 8 * g);
     }
     load_k(k0, pk);
     load_v(k0, pv);
   }
+  bool odd = false;  // some value that not all rows see is an infinity or NaN
   for (; k0 < hi; k0 += 128) {
-    int pk2 = 0, pv2 = 0;
     const bool more = k0 + 128 < hi;
-    if constexpr (PAGED)
-      if (more) {
-        pk2 = page_of(k0 + 128 + 8 * (c >> 2));
-        pv2 = page_of(k0 + 128 + 8 * g);
-      }
+    int pk3 = 0, pv3 = 0;
+    if constexpr (PAGED) {
+      pk3 = page_of(k0 + 256 + 8 * (c >> 2));
+      pv3 = page_of(k0 + 256 + 8 * g);
+    }
     // ---- scores
     float4_t s[NT][2];
 #pragma unroll
@@ -284,25 +291,20 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     if (more) load_k(k0 + 128, pk2);
     // ---- mask: key of score (t, i) is k0 + 8g + 4t + i
     const bool hole = PAGED && pv < 0;
-    const bool whole = k0 >= lo && k0 + 32 <= hi && (!p.causal || k0 + 31 <= p_first) &&
-                       (p.window == 0 || k0 > p_last - p.window) && !__any(hole);
-    uint32_t seen[NT];
+    const bool whole = whole_step(k0) && !__any(hole);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      seen[n] = 255u;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[n][t][i] *= p.scale_log2;
       if (!whole) {
-        seen[n] = 0u;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const bool ok = (uint32_t)(k0 + 8 * g + 4 * t + i - first[n]) < (hole ? 0u : (uint32_t)span[n]);
             s[n][t][i] = ok ? s[n][t][i] : -INFINITY;
-            seen[n] |= ok ? 1u << (4 * t + i) : 0u;
           }
       }
     }
@@ -338,87 +340,81 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
                         Half<BF16>::pack(pf[6], pf[7])};
     }
     // ---- values
-    uint32_t vp[8][DP];
+    if (!whole) {  // keys outside the range or in a hole: whatever is stored there counts as zero
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!whole) {  // keys outside the range or in a hole: whatever is stored there counts as zero
+      for (int i = 0; i < 8; ++i)
         if ((uint32_t)(k0 + 8 * g + i - lo) >= (hole ? 0u : (uint32_t)(hi - lo))) {
 #pragma unroll
           for (int x = 0; x < VW; ++x) vw[i][x] = 0u;
           if constexpr (CB < 16) vsc[i] = 127u;
         }
-      }
-      if constexpr (CB == 16) {
+    }
+    float vs[8];
 #pragma unroll
-        for (int x = 0; x < DP; ++x) vp[i][x] = vw[i][x];
-      } else {
-        const float sc = scale_of(vsc[i]);
-        if constexpr (DV == 4) {
-          if constexpr (CB == 8) {
-            vp[i][0] = Half<BF16>::template fp8<false>(vw[i][0], sc);
-            vp[i][1] = Half<BF16>::template fp8<true>(vw[i][0], sc);
-          } else {
-            vp[i][0] = Half<BF16>::template fp4<0>(vw[i][0], sc);
-            vp[i][1] = Half<BF16>::template fp4<1>(vw[i][0], sc);
-          }
-        } else {
+    for (int i = 0; i < 8; ++i) vs[i] = CB < 16 ? scale_of(vsc[i]) : 1.f;
+    // Infinities and NaN of values that some rows must not see are left out
+    // here (0 * inf would reach those rows through the product) and given to
+    // the rows that do see them below.
+    auto products = [&](auto clean) __attribute__((always_inline)) {
 #pragma unroll
-          for (int x = 0; x < DV / 8; ++x) {
-            const u32x4_t v = eight<BF16, CB>(vw[i], x, sc);
-            vp[i][4 * x] = v.x, vp[i][4 * x + 1] = v.y, vp[i][4 * x + 2] = v.z, vp[i][4 * x + 3] = v.w;
+      for (int x = 0; x < DP; ++x) {
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          u[i] = pair_at<BF16, CB>(vw[i], x, vs[i]);
+          if constexpr (decltype(clean)::value) {
+            odd = odd || odd_pair<BF16>(u[i]);
+            u[i] = finite_pair<BF16>(u[i]);
           }
         }
-      }
-    }
-    if (more) load_v(k0 + 128, pv2);
-    pk = pk2;
-    pv = pv2;
-    auto a_of = [&](int j) __attribute__((always_inline)) -> u32x4_t {
-      const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
-      u32x4_t a;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) a[x] = __builtin_amdgcn_perm(vp[2 * x + 1][j >> 1], vp[2 * x][j >> 1], sel);
-      return a;
+        for (int j = 0; j < 2; ++j) {
+          u32x4_t a;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) a[y] = __builtin_amdgcn_perm(u[2 * y + 1], u[2 * y], j ? 0x07060302u : 0x05040100u);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[n][2 * x + j] = Half<BF16>::mfma16(a, pr[n], o[n][2 * x + j]);
+        }
+      }
     };
-    bool odd = false;
-    if (!whole) {
+    if (whole) products(std::false_type{});
+    else products(std::true_type{});
+    if (more) load_v(k0 + 128, pv2);
+    pk = pk2, pv = pv2;
+    pk2 = pk3, pv2 = pv3;
+  }
+  if (__any(odd)) {
+    // rare: once more over the wave's steps that not all rows see whole
+#pragma unroll 1
+    for (int k = kr.start + 32 * wave; k < hi; k += 128) {
+#pragma unroll 1
+      for (int key = max(k, lo); key < min(k + 32, hi); ++key) {
+        const int pg = PAGED ? page_of(key) : 0;
+        if (pg < 0 || (whole_step(k) && !__any(PAGED && page_of(k + 8 * g) < 0))) continue;
+        const int64_t row = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i) {
+          const int d0 = DV * (4 * g + i);  // element i of operand j is dim d0 + j
+          uint32_t word[VW];
+          float scale = 1.f;
+          const uint8_t *a;
+          if constexpr (PAGED) {
+            a = p.cache.v + pg * p.cache.v_page + row * (D * CB / 8) + d0 * CB / 8;
+            if constexpr (CB < 16) scale = scale_of(p.cache.v_scale[pg * p.cache.vs_page + row * (D / 32) + d0 / 32]);
+          } else {
+            a = (const uint8_t *)(p.v.data + (int64_t)(w.q0 + key) * p.v.token + (int64_t)head * p.v.head + d0);
+          }
+          if constexpr (DV * CB < 32) word[0] = *(const uint16_t *)a;
+          else load_words(word, a);
 #pragma unroll
-        for (int x = 0; x < DP; ++x) odd = odd || odd_pair<BF16>(vp[i][x]);
-    }
-    if (__builtin_expect(!__any(odd), 1)) {
+          for (int x = 0; x < DP; ++x) {
+            const uint32_t u = pair_at<BF16, CB>(word, x, scale);
 #pragma unroll
-      for (int j = 0; j < DV; ++j) {
-        const u32x4_t a = a_of(j);
+            for (int j = 0; j < 2; ++j) {
+              const float f = Half<BF16>::up(j ? u >> 16 : u & 0xFFFFu);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][j] = Half<BF16>::mfma16(a, pr[n], o[n][j]);
-      }
-    } else {
-      // An infinity or NaN among values that some rows must not see: 0 * inf
-      // would reach them through the product.  The finite values take the
-      // product; then each class of the others is counted by a product of
-      // ones with what each row sees.
-#pragma unroll
-      for (int j = 0; j < DV; ++j) {
-        const u32x4_t a = a_of(j);
-        for (int cls = 0; cls < 4; ++cls) {
-          u32x4_t x;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) x[y] = class_pair<BF16>(a[y], cls);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (cls == 0) {
-              o[n][j] = Half<BF16>::mfma16(x, pr[n], o[n][j]);
-            } else {
-              constexpr uint32_t ONE = BF16 ? 0x3F80u : 0x3C00u;
-              u32x4_t b;
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                b[y] = ((seen[n] >> (2 * y)) & 1u) * ONE | (((seen[n] >> (2 * y + 1)) & 1u) * ONE) << 16;
-              const float4_t cnt = Half<BF16>::mfma16(x, b, (float4_t){0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[n][j][i] += odd_value(cnt[i], cls);
+              for (int n = 0; n < NT; ++n)
+                o[n][2 * x + j][i] += (uint32_t)(key - first[n]) < (uint32_t)span[n] && !__builtin_isfinite(f) ? f : 0.f;
             }
           }
         }
@@ -437,25 +433,18 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     }
   }
   __syncthreads();
-  // A tile whose keys are split writes its part to the workspace; the last of
-  // the tile's workgroups to arrive adds the parts up in their order, so the
-  // result does not depend on which one that is.
-  constexpr int PART = R * (D + 2);  // o as [n][wave][lane][DV], then m and the sum of each row
-  const bool split = w.splits > 1;
-  __amdgpu_buffer_rsrc_t rs;
-  if (split) rs = __builtin_amdgcn_make_buffer_rsrc(p.part + (int64_t)blockIdx.x * PART, (short)0, PART * 4, 0x00020000);
+  float top[NT], total[NT], mine[NT][DV];  // of element `wave` of the lane's operands
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float top = -INFINITY;
+    top[n] = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) top = __builtin_fmaxf(top, s_m[x][16 * n + c]);
+    for (int x = 0; x < 4; ++x) top[n] = __builtin_fmaxf(top[n], s_m[x][16 * n + c]);
     // a NaN score leaves top as the others' maximum, and its own sum NaN
-    const float base = top == -INFINITY ? 0.f : top;
-    float total = 0.f;
+    const float base = top[n] == -INFINITY ? 0.f : top[n];
+    total[n] = 0.f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) total += s_l[x][16 * n + c] * __builtin_amdgcn_exp2f(s_m[x][16 * n + c] - base);
+    for (int x = 0; x < 4; ++x) total[n] += s_l[x][16 * n + c] * __builtin_amdgcn_exp2f(s_m[x][16 * n + c] - base);
     const float keep = __builtin_amdgcn_exp2f(m[n] - base);
-    float mine[DV];
     for (int i = 0; i < 4; ++i) {
       __syncthreads();
 #pragma unroll
@@ -464,80 +453,84 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
       __syncthreads();
       if (wave == i) {
 #pragma unroll
-        for (int j = 0; j < DV; ++j) mine[j] = (s_o[0][lane][j] + s_o[1][lane][j]) + (s_o[2][lane][j] + s_o[3][lane][j]);
+        for (int j = 0; j < DV; ++j) mine[n][j] = (s_o[0][lane][j] + s_o[1][lane][j]) + (s_o[2][lane][j] + s_o[3][lane][j]);
       }
-    }
-    if (split) {
-#pragma unroll
-      for (int j = 0; j < DV; j += 4)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, (float4_t){mine[j], mine[j + 1], mine[j + 2], mine[j + 3]}),
-                                               rs, (((n * 4 + wave) * 64 + lane) * DV + j) * 4, 0, ATTN_CPOL_SC1);
-      if (wave == 0 && g == 0) {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), rs, (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(total), rs, (R * D + R + 16 * n + c) * 4, 0, ATTN_CPOL_SC1);
-      }
-    } else if (live[n]) {
-      store_row<BF16, DV>(p, w, r0 + 16 * n + c, head, DV * (4 * g + wave), mine, total);
     }
   }
-  if (!split) return;
-
-  __shared__ int s_last;
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // the wave's stores have been made (vmcnt 0)
-  __syncthreads();
-  uint32_t *counter = p.counters + w.slot * p.heads_kv + head;
-  if (threadIdx.x == 0)
-    s_last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)w.splits - 1u;
-  __syncthreads();
-  if (!s_last) return;
-  // parts of one tile and head lie heads_kv apart
-  float *first_part = p.part + ((int64_t)blockIdx.x - (int64_t)w.split * p.heads_kv) * PART;
-  const int64_t stride = (int64_t)p.heads_kv * PART;
-  constexpr int U = D == 256 ? 4 : 8;  // parts in flight
-  auto part_of = [&](int x) __attribute__((always_inline)) {
-    return __builtin_amdgcn_make_buffer_rsrc(first_part + x * stride, (short)0, PART * 4, 0x00020000);
-  };
+  if (w.splits > 1) {
+    // a part: o as [n][wave][lane][DV], then m and the sum of each row; rows
+    // that the tile does not have are neither written nor read
+    constexpr int PART = R * (D + 2);
+    auto part_of = [&](int x) __attribute__((always_inline)) {
+      return __builtin_amdgcn_make_buffer_rsrc(p.part + ((int64_t)(w.part - w.split + x) * p.heads_kv + head) * PART,
+                                               (short)0, PART * 4, 0x00020000);
+    };
+    auto put = [&](int x) __attribute__((always_inline)) {
+      const auto r = part_of(x);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float top = -INFINITY;
-    for (int x0 = 0; x0 < w.splits; x0 += 2 * U) {
-      float mx[2 * U];
+      for (int n = 0; n < NT; ++n) {
+        if (!live[n]) continue;
 #pragma unroll
-      for (int x = 0; x < 2 * U; ++x)
-        mx[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_of(min(x0 + x, w.splits - 1)),
-                                                                     (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
-#pragma unroll
-      for (int x = 0; x < 2 * U; ++x) top = __builtin_fmaxf(top, mx[x]);
-    }
-    const float base = top == -INFINITY ? 0.f : top;
-    float total = 0.f, acc[DV];
-#pragma unroll
-    for (int j = 0; j < DV; ++j) acc[j] = 0.f;
-    for (int x0 = 0; x0 < w.splits; x0 += U) {
-      float mx[U], lx[U];
-      float4_t ox[U][DV / 4];
-#pragma unroll
-      for (int x = 0; x < U; ++x) {
-        const auto r = part_of(min(x0 + x, w.splits - 1));
-        mx[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
-        lx[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (R * D + R + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
-#pragma unroll
-        for (int j = 0; j < DV / 4; ++j)
-          ox[x][j] = __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                      r, (((n * 4 + wave) * 64 + lane) * DV + 4 * j) * 4, 0, ATTN_CPOL_SC1));
-      }
-#pragma unroll
-      for (int x = 0; x < U; ++x)
-        if (x0 + x < w.splits) {
-          const float f = __builtin_amdgcn_exp2f(mx[x] - base);
-          total += lx[x] * f;
-#pragma unroll
-          for (int j = 0; j < DV; ++j) acc[j] += ox[x][j / 4][j % 4] * f;
+        for (int j = 0; j < DV; j += 4)
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(u32x4_t, (float4_t){mine[n][j], mine[n][j + 1], mine[n][j + 2], mine[n][j + 3]}), r,
+              (((n * 4 + wave) * 64 + lane) * DV + j) * 4, 0, ATTN_CPOL_SC1);
+        if (wave == 0 && g == 0) {
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top[n]), r, (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1);
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(total[n]), r, (R * D + R + 16 * n + c) * 4, 0,
+                                                ATTN_CPOL_SC1);
         }
-    }
-    if (live[n]) store_row<BF16, DV>(p, w, r0 + 16 * n + c, head, DV * (4 * g + wave), acc, total);
+      }
+    };
+    auto add = [&](int x0, int count, int step) __attribute__((always_inline)) {
+      constexpr int U = PART_FAN;  // parts in flight
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        top[n] = -INFINITY;
+        total[n] = 0.f;
+#pragma unroll
+        for (int j = 0; j < DV; ++j) mine[n][j] = 0.f;
+        if (!live[n]) continue;
+#pragma unroll 1
+        for (int x = 0; x < count; x += U) {
+          float mx[U], lx[U];
+          float4_t ox[U][DV / 4];
+          float grown = top[n];
+#pragma unroll
+          for (int y = 0; y < U; ++y) {
+            const auto r = part_of(x0 + min(x + y, count - 1) * step);
+            mx[y] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (R * D + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
+            lx[y] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (R * D + R + 16 * n + c) * 4, 0, ATTN_CPOL_SC1));
+#pragma unroll
+            for (int j = 0; j < DV / 4; ++j)
+              ox[y][j] = __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                          r, (((n * 4 + wave) * 64 + lane) * DV + 4 * j) * 4, 0, ATTN_CPOL_SC1));
+          }
+#pragma unroll
+          for (int y = 0; y < U; ++y) grown = __builtin_fmaxf(grown, mx[y]);
+          const float base = grown == -INFINITY ? 0.f : grown;
+          const float keep = __builtin_amdgcn_exp2f(top[n] - base);
+          top[n] = grown;
+          total[n] *= keep;
+#pragma unroll
+          for (int j = 0; j < DV; ++j) mine[n][j] *= keep;
+#pragma unroll
+          for (int y = 0; y < U; ++y)
+            if (x + y < count) {
+              const float f = __builtin_amdgcn_exp2f(mx[y] - base);
+              total[n] += lx[y] * f;
+#pragma unroll
+              for (int j = 0; j < DV; ++j) mine[n][j] += ox[y][j / 4][j % 4] * f;
+            }
+        }
+      }
+    };
+    put(w.split);
+    if (!add_parts(p, w, head, add, put)) return;
   }
-  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    if (live[n]) store_row<BF16, DV>(p, w, r0 + 16 * n + c, head, DV * (4 * g + wave), mine[n], total[n]);
 }
 
 }  // namespace exl3

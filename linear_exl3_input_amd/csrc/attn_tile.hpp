@@ -41,15 +41,6 @@ __device__ __forceinline__ float16_t mfma32(u32x4_t a, u32x4_t b, float16_t c) {
                                                   0, 0);
 }
 
-// A pair of 16-bit values with infinities and NaN replaced by 0.
-template <bool BF16>
-__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
-  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u;
-  if ((x & E) == E) x &= 0xFFFF0000u;
-  if (((x >> 16) & E) == E) x &= 0xFFFFu;
-  return x;
-}
-
 // The larger (the sum) of a lane's value and its partner's, 32 lanes on.
 __device__ __forceinline__ float pair_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -88,28 +79,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int head = blockIdx.x % p.heads_kv;
   const int item = blockIdx.x / p.heads_kv;
   Work w;
-  int C;
-  if (!find_work<R>(p, item, lane, w, C)) return;
+  if (!find_work<R>(p, item, lane, w)) return;
   const int rows = w.q_len * p.group;
   {
     // a sequence's last tiles have the most keys and go first
     const int tiles = (rows + R - 1) / R;
-    const int turned = tiles - 1 - w.tile;
-    w.slot += turned - w.tile;
-    w.tile = turned;
+    w.tile = tiles - 1 - w.tile;
   }
 
   // ---- the tile's rows and their keys
   const int r0 = w.tile * R;
   const int r_last = min(r0 + R, rows) - 1;
-  const int shift = w.kv_len - w.q_len;
-  const int p_first = shift + r0 / p.group, p_last = shift + r_last / p.group;
-  const int hi_all = p.causal ? min(w.kv_len, p_last + 1) : w.kv_len;
-  const int lo_all = p.window > 0 ? max(0, p_first - p.window + 1) : 0;
-  const int64_t from = (int64_t)(lo_all & ~31) + (int64_t)w.split * C;
-  const int lo = (int)min<int64_t>(max<int64_t>(from, lo_all), 0x7FFFFF00);
-  const int hi = (int)min<int64_t>(from + C, hi_all);
-  const int start = lo & ~31;
+  const KeyRange kr = key_range(p, w, r0, r_last);
+  const int lo = kr.lo, hi = kr.hi, p_first = kr.p_first, p_last = kr.p_last, shift = kr.shift;
+  const int start = kr.start;
   const int n_tiles = hi > lo ? (hi - start + BN - 1) / BN : 0;
 
   // ---- the lane's row
@@ -390,65 +373,65 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
       store_row<BF16, 8>(p, w, r, head, 8 * piece_of(x), v, l);
     }
   };
-  if (w.splits == 1) {
-    store_rows();
-    return;
-  }
-  // ---- parts, as in attn_small_kernel: [wave][o register][lane], then m and
-  // the sum of each row
-  constexpr int PART = R * (D + 2);
-  constexpr int OV = 16 * DT;
-  const auto rs = __builtin_amdgcn_make_buffer_rsrc(p.part + (int64_t)blockIdx.x * PART, (short)0, PART * 4, 0x00020000);
+  if (w.splits > 1) {
+    // a part: [wave][o register / 4][lane][4], then m and the sum of each row
+    constexpr int PART = R * (D + 2);
+    constexpr int OV = 4 * DT;
+    const bool any = r0 + 32 * wave < rows;  // the wave has rows
+    auto part_of = [&](int x) __attribute__((always_inline)) {
+      return __builtin_amdgcn_make_buffer_rsrc(p.part + ((int64_t)(w.part - w.split + x) * p.heads_kv + head) * PART,
+                                               (short)0, PART * 4, 0x00020000);
+    };
+    auto put = [&](int x) __attribute__((always_inline)) {
+      if (!any) return;
+      const auto rs = part_of(x);
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-    for (int y = 0; y < 4; ++y)
-      __builtin_amdgcn_raw_buffer_store_b128(
-          __builtin_bit_cast(u32x4_t, (float4_t){o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]}), rs,
-          ((wave * (OV / 4) + 4 * d + y) * 64 + lane) * 16, 0, ATTN_CPOL_SC1);
-  if (h == 0) {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), rs, (R * D + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), rs, (R * D + R + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1);
-  }
-  __shared__ int s_last;
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // the wave's stores have been made (vmcnt 0)
-  __syncthreads();
-  uint32_t *counter = p.counters + w.slot * p.heads_kv + head;
-  if (tid == 0)
-    s_last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)w.splits - 1u;
-  __syncthreads();
-  if (!s_last) return;
-  float *first_part = p.part + ((int64_t)blockIdx.x - (int64_t)w.split * p.heads_kv) * PART;
-  auto part_of = [&](int x) __attribute__((always_inline)) {
-    return __builtin_amdgcn_make_buffer_rsrc(first_part + (int64_t)x * p.heads_kv * PART, (short)0, PART * 4, 0x00020000);
-  };
-  float top = -INFINITY;
-  for (int x = 0; x < w.splits; ++x)
-    top = __builtin_fmaxf(top, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                                   part_of(x), (R * D + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1)));
-  const float base = top == -INFINITY ? 0.f : top;
-  l = 0.f;
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  for (int x = 0; x < w.splits; ++x) {
-    const auto rx = part_of(x);
-    const float f = __builtin_amdgcn_exp2f(
-        __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rx, (R * D + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1)) - base);
-    l += f * __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rx, (R * D + R + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1));
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float4_t v = __builtin_bit_cast(
-            float4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, ((wave * (OV / 4) + 4 * d + y) * 64 + lane) * 16, 0, ATTN_CPOL_SC1));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[d][4 * y + i] += v[i] * f;
+        for (int y = 0; y < 4; ++y)
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(u32x4_t, (float4_t){o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]}), rs,
+              ((wave * OV + 4 * d + y) * 64 + lane) * 16, 0, ATTN_CPOL_SC1);
+      if (h == 0) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m), rs, (R * D + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(l), rs, (R * D + R + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1);
       }
+    };
+    auto add = [&](int x0, int count, int step) __attribute__((always_inline)) {
+      m = -INFINITY;
+      l = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+      if (!any) return;
+      auto row_of = [&](int x, int which) __attribute__((always_inline)) {
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_of(x0 + x * step), (R * D + which * R + 32 * wave + col) * 4,
+                                                                    0, ATTN_CPOL_SC1));
+      };
+#pragma unroll 4
+      for (int x = 0; x < count; ++x) m = __builtin_fmaxf(m, row_of(x, 0));
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+      for (int x = 0; x < count; ++x) {
+        const auto rs = part_of(x0 + x * step);
+        const float f = __builtin_amdgcn_exp2f(row_of(x, 0) - base);
+        l += f * row_of(x, 1);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float4_t v = __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                rs, ((wave * OV + 4 * d + y) * 64 + lane) * 16, 0, ATTN_CPOL_SC1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][4 * y + i] += v[i] * f;
+          }
+      }
+    };
+    put(w.split);
+    if (!add_parts(p, w, head, add, put)) return;
   }
   store_rows();
-  if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 }  // namespace exl3
