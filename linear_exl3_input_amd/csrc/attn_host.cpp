@@ -469,6 +469,11 @@ exl3_status exl3_prompt_attention(const exl3_rows *q, const exl3_rows *k, const 
   if ((st = check_rows(out, "out", tokens, head_dim, true)) != EXL3_OK) return st;
   if (q->heads != out->heads)
     return host_fail(EXL3_ERR_INVALID_ARG, "out has %d heads, q %d", out->heads, q->heads);
+  // tiles of up to 128 keys are addressed with 32-bit offsets
+  constexpr int64_t MAX_TOKEN_STRIDE = 1 << 22;
+  if (k->token_stride > MAX_TOKEN_STRIDE || v->token_stride > MAX_TOKEN_STRIDE)
+    return host_fail(EXL3_ERR_UNSUPPORTED, "token strides of k (%lld) and v (%lld) must be at most %lld elements",
+                     (long long)k->token_stride, (long long)v->token_stride, (long long)MAX_TOKEN_STRIDE);
   if (k->heads != v->heads) return host_fail(EXL3_ERR_INVALID_ARG, "k has %d heads, v %d", k->heads, v->heads);
   if ((st = check_attention_sizes(batch, tokens, q->heads, k->heads)) != EXL3_OK) return st;
   if (causal != 0 && causal != 1) return host_fail(EXL3_ERR_INVALID_ARG, "causal=%d, must be 0 or 1", causal);

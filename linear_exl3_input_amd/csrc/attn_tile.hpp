@@ -74,7 +74,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   __shared__ __align__(16) uint8_t lds[2 * G::BUF];
   __shared__ int s_odd;  // some tile that not all rows see whole has infinities or NaN among its values
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: a wave stages keys or values
   const int col = lane & 31, h = lane >> 5;
   const int head = blockIdx.x % p.heads_kv;
   const int item = blockIdx.x / p.heads_kv;
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   }
 
   // ---- staging: thread's block of a tile is rows 8a .. 8a+7, piece c
-  const bool stage_v = tid >= 128;
+  const bool stage_v = wave >= 2;
   const int st = tid & 127;
   const int c = st % NC, a8 = 8 * (st / NC);
   const int ps_mask = (1 << p.cache.page_shift) - 1;
@@ -155,10 +156,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
         for (int i = 0; i < 8; ++i) sc[i] = s[i * (D / 32)];
       }
     } else {
-      const Rows src = stage_v ? p.v : p.k;
-      const uint16_t *a = src.data + (int64_t)head * src.head + 8 * c;
+      // rows past the last key read as zeros
+      const int64_t token = stage_v ? p.v.token : p.k.token;
+      const uint16_t *a = (stage_v ? p.v.data + head * p.v.head : p.k.data + head * p.k.head) +
+                          (int64_t)(w.q0 + start + t * BN) * token;
+      const int step = (int)token * 2;  // the host keeps a tile's rows within 2^31 bytes
+      const auto rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t *>(a), (short)0, (min(hi - start - t * BN, BN) - 1) * step + D * 2, 0x00020000);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) load_words(raw[i], (const uint8_t *)(a + (int64_t)(w.q0 + min(key + i, hi - 1)) * src.token));
+      for (int i = 0; i < 8; ++i) {
+        const u32x4_t x = __builtin_amdgcn_raw_buffer_load_b128(rs, a8 * step + c * 16, i * step, 0);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) raw[i][y] = x[y];
+      }
     }
   };
   // whether every row of the workgroup sees every key of tile t
