@@ -31,6 +31,11 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", f"--offload-arch={A
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-I", os.path.join(ROOT, "include"), "-Wno-unused-command-line-argument"]
 
+# The attention kernels' scores are matrix products that vector instructions
+# read, so products write VGPRs; left alone, the compiler gives kernels with
+# more than 256 registers a wave AGPR results and copies every one.
+EXTRA = {f"attn_d{d}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for d in (64, 128, 256)}
+
 
 def _hipcc() -> str:
     for cand in (shutil.which("hipcc"), "/opt/rocm/bin/hipcc"):
@@ -57,7 +62,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
-        cmds.append([hipcc, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj])
+        cmds.append([hipcc, *COMMON, *EXTRA.get(src, ()), "-c", os.path.join(CSRC, src), "-o", obj])
     jobs = jobs or min(8, os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         for out in ex.map(_run, cmds):

@@ -151,7 +151,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
   auto seq_at = [&](int s0) __attribute__((always_inline)) { return s0 == 0 ? head : load(s0 + lane); };
   int C = 0x7FFFFFFF;
   auto splits_of = [&](const Seq &x) __attribute__((always_inline)) -> int {
-    return x.span > C ? (int)(((int64_t)x.span + C - 1) / C) : 1;
+    return x.span > C ? (int)(((uint32_t)x.span + (uint32_t)C - 1u) / (uint32_t)C) : 1;
   };
   if (p.target > 0) {
     // in floats, whose rounding the last factor more than covers: C is never

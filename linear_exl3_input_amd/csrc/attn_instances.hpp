@@ -31,7 +31,7 @@ hipError_t small_bits(int bits, const AttnParams &p, hipStream_t s) {
 
 template <bool BF16, int BITS>
 hipError_t tile_of(const AttnParams &p, hipStream_t s) {
-  const dim3 grid((unsigned)(grid_items(p, TileGeom<EXL3_HEAD_DIM>::ROWS) * p.heads_kv));
+  const dim3 grid((unsigned)(grid_items(p, ATTN_TILE_ROWS) * p.heads_kv));
   hipLaunchKernelGGL((attn_tile_kernel<BF16, EXL3_HEAD_DIM, BITS>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }

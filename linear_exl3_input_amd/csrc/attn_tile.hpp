@@ -53,7 +53,6 @@ __device__ __forceinline__ float pair_sum(float v) {
 
 template <int D>
 struct TileGeom {
-  static constexpr int ROWS = ATTN_TILE_ROWS;  // query rows of a workgroup
   static constexpr int BN = 8192 / D;       // keys of a tile
   static constexpr int NS = BN / 32;        // 32-key products
   static constexpr int NC = D / 8;          // 16-byte pieces of a row
@@ -69,7 +68,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   using G = TileGeom<D>;
   constexpr bool PAGED = BITS != 0;
   constexpr int CB = PAGED ? BITS : 16;
-  constexpr int R = G::ROWS, BN = G::BN, NS = G::NS, NC = G::NC, DT = G::DT;
+  constexpr int R = ATTN_TILE_ROWS, BN = G::BN, NS = G::NS, NC = G::NC, DT = G::DT;
   constexpr int PW = CB / 4;  // words of 8 values: 4, 2 or 1
   __shared__ __align__(16) uint8_t lds[2 * G::BUF];
   __shared__ int s_odd;  // some tile that not all rows see whole has infinities or NaN among its values
@@ -96,21 +95,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int start = kr.start;
   const int n_tiles = hi > lo ? (hi - start + BN - 1) / BN : 0;
 
-  // ---- the lane's row
-  const int r = r0 + 32 * wave + col;
-  const bool live = r < rows;
-  const int tok = (live ? r : r_last) / p.group;
-  const int qh = (live ? r : r_last) - tok * p.group;
+  // ---- the lane's row, which sees the keys first .. first + span - 1
+  const int row = r0 + 32 * wave + col;
+  const bool live = row < rows;
+  const int tok = (live ? row : r_last) / p.group;
+  const int qh = (live ? row : r_last) - tok * p.group;
   const int pos = shift + tok;
   const int first = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
   const int span = max(0, (p.causal ? min(hi, pos + 1) : hi) - first);
-  // of the wave's rows: every one sees [w_lo, w_hi), none beyond w_end
-  const int wr0 = min(r0 + 32 * wave, r_last), wr1 = min(wr0 + 31, r_last);
-  const int wp0 = shift + wr0 / p.group, wp1 = shift + wr1 / p.group;
-  const int w_hi = p.causal ? min(hi, wp0 + 1) : hi, w_end = p.causal ? min(hi, wp1 + 1) : hi;
-  const int w_lo = p.window > 0 ? max(lo, wp1 - p.window + 1) : lo;
-  const int w_from = p.window > 0 ? max(lo, wp0 - p.window + 1) : lo;
-
+  // of the wave's rows, first to last, every one sees [w_lo, w_hi)
+  const int wp0 = shift + min(r0 + 32 * wave, r_last) / p.group;
+  const int wp1 = shift + min(r0 + 32 * wave + 31, r_last) / p.group;
+  const int w_hi = p.causal ? min(hi, wp0 + 1) : hi, w_lo = p.window > 0 ? max(lo, wp1 - p.window + 1) : lo;
   u32x4_t q[D / 16];
   {
     const uint16_t *a = p.q.data + (int64_t)(w.q0 + tok) * p.q.token + (int64_t)(head * p.group + qh) * p.q.head + 8 * h;
@@ -118,10 +114,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     for (int s = 0; s < D / 16; ++s) q[s] = *(const u32x4_t *)(a + 16 * s);
   }
 
-  // ---- staging: thread's block of a tile is rows 8a .. 8a+7, piece c
-  const bool stage_v = wave >= 2;
-  const int st = tid & 127;
-  const int c = st % NC, a8 = 8 * (st / NC);
+  // ---- staging: of every tile a thread has piece c (8 dims) of the keys
+  // ka .. ka+3 and half of piece c of the values of va .. va+7
+  const int c = tid % NC;
+  const int ka = 4 * (tid / NC), va = 8 * (tid / (2 * NC));
+  const int half = (tid / NC) & 1;
   const int ps_mask = (1 << p.cache.page_shift) - 1;
   const int32_t *table = PAGED ? p.page_table + (int64_t)w.seq * p.table_stride : nullptr;
   auto page_of = [&](int key) __attribute__((always_inline)) -> int {
@@ -130,6 +127,72 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     if (key < hi && i < p.table_width) pg = table[i];
     return pg >= 0 && pg < p.cache.pages ? pg : -1;
   };
+  constexpr int HW = CB == 4 ? 1 : CB / 8;  // words of half a piece (of 4 bits: two bytes)
+  constexpr int ROW = D * CB / 8;           // bytes of a cached row
+  uint32_t kraw[4][PW], vraw[8][HW];
+  uint32_t ksc[4], vsc[8];
+  // Packed rows: a descriptor that ends with tile t's last key, so rows past it
+  // read as zeros (and nothing is read past the last tile).
+  auto packed = [&](const Rows &x, int t) __attribute__((always_inline)) {
+    const int n = min(hi - start - t * BN, BN);  // the host keeps a tile's rows within 2^31 bytes
+    return __builtin_amdgcn_make_buffer_rsrc(x.data + head * x.head + (int64_t)(w.q0 + start + t * BN) * x.token, (short)0,
+                                             n > 0 ? (n - 1) * ((int)x.token * 2) + D * 2 : 0, 0x00020000);
+  };
+  // The loads of keys tk and values tv, in 12 pieces (4 of keys, 8 of values)
+  // for the caller to spread; a page that is none reads page 0, its keys are
+  // masked and its values zeroed.
+  auto fetch = [&](int tk, int kpg, int tv, int vpg) __attribute__((always_inline)) {
+    if constexpr (PAGED) {
+      const int64_t kat = ((int64_t)head << p.cache.page_shift) + ((start + tk * BN + ka) & ps_mask);
+      const int64_t vat = ((int64_t)head << p.cache.page_shift) + ((start + tv * BN + va) & ps_mask);
+      const uint8_t *k = p.cache.k + max(kpg, 0) * p.cache.k_page + kat * ROW + c * CB;
+      const uint8_t *v = p.cache.v + max(vpg, 0) * p.cache.v_page + vat * ROW + c * CB + half * (CB / 2);
+      const uint8_t *ks = nullptr, *vs = nullptr;
+      if constexpr (CB < 16) {
+        ks = p.cache.k_scale + max(kpg, 0) * p.cache.ks_page + kat * (D / 32) + (c >> 2);
+        vs = p.cache.v_scale + max(vpg, 0) * p.cache.vs_page + vat * (D / 32) + (c >> 2);
+      }
+      return [&, k, v, ks, vs](int i) __attribute__((always_inline)) {
+        if (i < 4) {
+          load_words(kraw[i], k + i * ROW);
+          if constexpr (CB < 16) ksc[i] = ks[i * (D / 32)];
+        } else {
+          i -= 4;
+          if constexpr (CB == 4) vraw[i][0] = *(const uint16_t *)(v + i * ROW);
+          else load_words(vraw[i], v + i * ROW);
+          if constexpr (CB < 16) vsc[i] = vs[i * (D / 32)];
+        }
+      };
+    } else {
+      const auto krs = packed(p.k, tk), vrs = packed(p.v, tv);
+      const int kstep = (int)p.k.token * 2, vstep = (int)p.v.token * 2;
+      return [&, krs, vrs, kstep, vstep](int i) __attribute__((always_inline)) {
+        if (i < 4) {
+          const u32x4_t x = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(krs, ka * kstep + c * 16, i * kstep, 0));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) kraw[i][y] = x[y];
+        } else {
+          i -= 4;
+          const u32x2_t x = __builtin_bit_cast(
+              u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(vrs, va * vstep + c * 16 + half * 8, i * vstep, 0));
+          vraw[i][0] = x.x, vraw[i][HW - 1] = x.y;
+        }
+      };
+    }
+  };
+  // The first loads, and while they are on their way a look at every page for
+  // holes and the wait for q (which inside the loop would also be one for the
+  // tiles on their way).
+  auto key_page = [&](int t, int a) __attribute__((always_inline)) { return PAGED ? page_of(start + t * BN + a) : 0; };
+  int vpg = key_page(0, va);  // of the values in vraw
+  int kpg_next = key_page(0, ka), vpg_next = key_page(1, va);
+  if (n_tiles > 0) {
+    const auto load = fetch(0, kpg_next, 0, vpg);
+    kpg_next = key_page(1, ka);
+#pragma unroll
+    for (int i = 0; i < 12; ++i) load(i);
+  }
   if (tid == 0) s_odd = 0;
   bool holes = false;
   if constexpr (PAGED) {
@@ -137,83 +200,64 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     for (int i = (start >> p.cache.page_shift) + tid; ((int64_t)i << p.cache.page_shift) < hi; i += 256)
       any |= page_of(max(i << p.cache.page_shift, start)) < 0;
     holes = __syncthreads_or(any) != 0;
+  } else {
+    __syncthreads();
   }
-  uint32_t raw[8][PW];
-  uint32_t sc[8];
-  auto fetch = [&](int t, int pg) __attribute__((always_inline)) {
-    const int key = start + t * BN + a8;
-    if constexpr (PAGED) {
-      const int pi = max(pg, 0);  // a hole reads page 0; its keys are masked and its values zeroed
-      const int64_t row = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
-      const uint8_t *a = (stage_v ? p.cache.v + pi * p.cache.v_page : p.cache.k + pi * p.cache.k_page) +
-                         row * (D * CB / 8) + c * CB;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) load_words(raw[i], a + i * (D * CB / 8));
-      if constexpr (CB < 16) {
-        const uint8_t *s = (stage_v ? p.cache.v_scale + pi * p.cache.vs_page : p.cache.k_scale + pi * p.cache.ks_page) +
-                           row * (D / 32) + (c >> 2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sc[i] = s[i * (D / 32)];
-      }
-    } else {
-      // rows past the last key read as zeros
-      const int64_t token = stage_v ? p.v.token : p.k.token;
-      const uint16_t *a = (stage_v ? p.v.data + head * p.v.head : p.k.data + head * p.k.head) +
-                          (int64_t)(w.q0 + start + t * BN) * token;
-      const int step = (int)token * 2;  // the host keeps a tile's rows within 2^31 bytes
-      const auto rs = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint16_t *>(a), (short)0, (min(hi - start - t * BN, BN) - 1) * step + D * 2, 0x00020000);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const u32x4_t x = __builtin_amdgcn_raw_buffer_load_b128(rs, a8 * step + c * 16, i * step, 0);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) raw[i][y] = x[y];
-      }
-    }
-  };
+  for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(q[s]));
   // whether every row of the workgroup sees every key of tile t
   auto whole_tile = [&](int t) __attribute__((always_inline)) {
     const int k0 = start + t * BN;
     return k0 >= lo && k0 + BN <= hi && (!p.causal || k0 + BN - 1 <= p_first) &&
            (p.window == 0 || k0 > p_last - p.window) && !holes;
   };
-  auto put = [&](int t, int pg) __attribute__((always_inline)) {
-    uint8_t *buf = lds + (t & 1) * G::BUF;
-    u32x4_t x[8];
+  // Piece i (0..3) of the thread's keys to tile t's buffer.
+  auto put_k = [&](int t, int i) __attribute__((always_inline)) {
+    // key 16t + 8h + 4u + i of each 32 to row 16t + 8u + 4h + i
+    const int at = (ka & ~12) | ((ka & 8) >> 1) | ((ka & 4) << 1);
+    *(u32x4_t *)(lds + (t & 1) * G::BUF + c * G::K_PIECE + (at + i) * 16) =
+        eight<BF16, CB>(kraw[i], 0, CB < 16 ? scale_of(ksc[i]) : 1.f);
+  };
+  // Values of a tile that some row does not see whole: what lies outside the
+  // range or in a hole counts as zero, and so do infinities and NaN that some
+  // rows must not see (0 * inf would reach them through the product); the rows
+  // that do see them get them at the end.
+  auto clean_v = [&](int t, int pg) __attribute__((always_inline)) {
+    bool odd = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = eight<BF16, CB>(raw[i], 0, CB < 16 ? scale_of(sc[i]) : 1.f);
-    if (!stage_v) {
-      // key 16t + 8h + 4u + i of each 32 to row 16t + 8u + 4h + i
-      const int row = (a8 & ~31) | (a8 & 16) | ((a8 & 8) >> 1);
+    for (int i = 0; i < 8; ++i) {
+      const bool in = (uint32_t)(start + t * BN + va + i - lo) < (uint32_t)(hi - lo) && (!PAGED || pg >= 0);
+      if constexpr (CB < 16) {
+        const bool bad = vsc[i] == 255u;  // the only codes that are not finite
+        odd = odd || (in && bad);
+        if (!in || bad) {
+          vsc[i] = 127u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *(u32x4_t *)(buf + c * G::K_PIECE + (row + (i & 3) + 2 * (i & 4)) * 16) = x[i];
-    } else {
-      if (!whole_tile(t)) {
-        // what lies outside the range or in a hole counts as zero, and so do
-        // infinities and NaN that some rows must not see (0 * inf would reach
-        // them through the product); the rows that do see them get them below
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool in = (uint32_t)(start + t * BN + a8 + i - lo) < (uint32_t)(hi - lo) && (!PAGED || pg >= 0);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            x[i][y] = in ? x[i][y] : 0u;
-            odd = odd || odd_pair<BF16>(x[i][y]);
-            x[i][y] = finite_pair<BF16>(x[i][y]);
-          }
+          for (int y = 0; y < HW; ++y) vraw[i][y] = 0u;
         }
-        if (odd) s_odd = 1;
-      }
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
-        u32x4_t y;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) y[z] = __builtin_amdgcn_perm(x[2 * z + 1][j >> 1], x[2 * z][j >> 1], sel);
-        *(u32x4_t *)(buf + G::K_BYTES + ((a8 >> 3) * D + j * NC + c) * 16) = y;
+        for (int y = 0; y < HW; ++y) {
+          vraw[i][y] = in ? vraw[i][y] : 0u;
+          odd = odd || odd_pair<BF16>(vraw[i][y]);
+          vraw[i][y] = finite_pair<BF16>(vraw[i][y]);
+        }
       }
+    }
+    if (odd) s_odd = 1;
+  };
+  // Dims 2j and 2j + 1 (j 0..1) of the thread's values, keys side by side.
+  auto put_v = [&](int t, int j) __attribute__((always_inline)) {
+    uint32_t x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = pair_at<BF16, CB>(vraw[i], j, CB < 16 ? scale_of(vsc[i]) : 1.f);
+    uint8_t *buf = lds + (t & 1) * G::BUF + G::K_BYTES + ((va >> 3) * D + 4 * half * NC + c) * 16;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      u32x4_t v;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) v[z] = __builtin_amdgcn_perm(x[2 * z + 1], x[2 * z], y ? 0x07060302u : 0x05040100u);
+      *(u32x4_t *)(buf + (2 * j + y) * NC * 16) = v;
     }
   };
 
@@ -223,112 +267,182 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float m = -INFINITY, l = 0.f;  // m: in units of log2, as the scores times scale_log2
+  float16_t s[NS];    // scores
+  u32x4_t pr[NS][2];  // probabilities in the type
+  constexpr int READS = 16;  // LDS reads of either product of a tile
+  constexpr int AHEAD = 3;   // that many are made before their products
 
-  if (n_tiles > 0) {
-    int pg = PAGED ? page_of(start + a8) : 0;
-    fetch(0, pg);
-    __syncthreads();
-    put(0, pg);
-    if (n_tiles > 1) {
-      pg = PAGED ? page_of(start + BN + a8) : 0;
-      fetch(1, pg);
+  // Tile t's scores, and beside the products the staging of keys t + 1 and
+  // values t.  Here and below a step is what is between two scheduling
+  // barriers: operands are read AHEAD steps before their products, and the
+  // rest is spread so that no step waits for itself or crowds the LDS or the
+  // memory path.
+  auto score_and_stage = [&](int t) __attribute__((always_inline)) {
+    const uint8_t *kb = lds + (t & 1) * G::BUF + h * G::K_PIECE + col * 16;
+    auto read = [&](int x) __attribute__((always_inline)) {  // the keys of product x = d * NS + n
+      return *(const u32x4_t *)(kb + 2 * (x / NS) * G::K_PIECE + 32 * (x % NS) * 16);
+    };
+    u32x4_t ring[READS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[n][i] = 0.f;
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) ring[x] = read(x);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < READS; ++x) {
+      if (x + AHEAD < READS) ring[x + AHEAD] = read(x + AHEAD);
+      s[x % NS] = mfma32<BF16>(ring[x], q[x / NS], s[x % NS]);
+      if (x >= 2 && x < 10 && x % 2 == 0) put_k(t + 1, (x - 2) / 2);
+      if (x == 3 || x == 7) put_v(t, x / 4);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
-    for (int t = 0; t < n_tiles; ++t) {
-      if (t + 1 < n_tiles) {
-        put(t + 1, pg);
-        if (t + 2 < n_tiles) {
-          pg = PAGED ? page_of(start + (t + 2) * BN + a8) : 0;
-          fetch(t + 2, pg);
+  };
+  // The mask, and the running maximum: it moves only when some row's grew by
+  // more than 2^8, so probabilities reach at most 2^8 (within range for both
+  // types, and the sums are fp32).  True when it did: o then has to be
+  // multiplied by `keep`.
+  auto settle = [&](int t, float &keep) __attribute__((always_inline)) -> bool {
+    const int k0 = start + t * BN;
+    if (!(k0 >= w_lo && k0 + BN <= w_hi && !holes)) {
+      // element 8t8 + i of product n is key k0 + 32n + 16t8 + 8h + i
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int t8 = 0; t8 < 2; ++t8) {
+          const int key = k0 + 32 * n + 16 * t8 + 8 * h;
+          const uint32_t seen = PAGED && holes && page_of(key) < 0 ? 0u : (uint32_t)span;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s[n][8 * t8 + i] = (uint32_t)(key + i - first) < seen ? s[n][8 * t8 + i] : -INFINITY;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[n][i]);
+    top = pair_max(top) * p.scale_log2;
+    if (!__any(top > m + 8.f)) return false;
+    const float grown = __builtin_fmaxf(m, top);
+    keep = grown == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - grown);
+    m = grown;
+    l *= keep;
+    return true;
+  };
+  // o += the product of tile t's probabilities and values.
+  auto product = [&](int t) __attribute__((always_inline)) {
+    const uint8_t *vb = lds + (t & 1) * G::BUF + G::K_BYTES + col * 16;
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int t8 = 0; t8 < 2; ++t8)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const u32x4_t a = *(const u32x4_t *)(vb + ((4 * n + 2 * t8 + h) * D + 32 * d) * 16);
+          o[d] = mfma32<BF16>(a, pr[n][t8], o[d]);
+        }
+  };
+  // Probabilities are rounded to the type for the product (an error no larger
+  // than the output's own rounding); the sum takes them unrounded.
+  auto weigh = [&]() __attribute__((always_inline)) {
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int t8 = 0; t8 < 2; ++t8) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][8 * t8 + i], p.scale_log2, -base));
+          l += e[i];
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) pr[n][t8][y] = Half<BF16>::pack(e[2 * y], e[2 * y + 1]);
+      }
+  };
+  // product(t) with weigh() of the next tile and the loads beside it: in each
+  // step a product, and of the vector work one group's scores scaled, the last
+  // group's exponentials, and the sum and packing of the one before.
+  auto product_and_weigh = [&](int t, auto load) __attribute__((always_inline)) {
+    const uint8_t *vb = lds + (t & 1) * G::BUF + G::K_BYTES + col * 16;
+    auto read = [&](int x) __attribute__((always_inline)) {  // the values of product x = (2n + t8) * DT + d
+      return *(const u32x4_t *)(vb + ((2 * (x / DT) + h) * D + 32 * (x % DT)) * 16);
+    };
+    u32x4_t ring[READS];
+    u32x4_t was[NS][2];
+    float f[16 * NS], sum[2] = {0.f, 0.f};
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) was[n][0] = pr[n][0], was[n][1] = pr[n][1];
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) ring[x] = read(x);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < READS + 2; ++x) {
+      if (x + AHEAD < READS) ring[x + AHEAD] = read(x + AHEAD);
+      if (x >= 2 && x < 14) load(x - 2);
+      if (x < READS) o[x % DT] = mfma32<BF16>(ring[x], was[x / DT / 2][x / DT % 2], o[x % DT]);
+#pragma unroll
+      for (int g = 0; g < NS; ++g) {
+        const int e0 = x * NS + g, e1 = e0 - NS, e2 = e1 - NS;
+        if (x < READS) f[e0] = __builtin_fmaf(s[e0 / 16][e0 % 16], p.scale_log2, -base);
+        if (x >= 1 && x <= READS) f[e1] = __builtin_amdgcn_exp2f(f[e1]);
+        if (x >= 2) {
+          sum[e2 & 1] += f[e2];
+          if (e2 & 1) pr[e2 / 16][e2 / 8 % 2][e2 / 2 % 4] = Half<BF16>::pack(f[e2 - 1], f[e2]);
         }
       }
-      const int k0 = start + t * BN;
-      const uint8_t *buf = lds + (t & 1) * G::BUF;
-      if (k0 < w_end && k0 + BN > w_from) {
-        // ---- scores
-        float16_t s[NS];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    l += sum[0] + sum[1];
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+    for (int n = 0; n < NS; ++n) asm volatile("" : "+v"(pr[n][0]), "+v"(pr[n][1]));  // made here, not where they are used
+  };
+
+  if (n_tiles > 0) {
+    // Turn t reads keys t and values t - 1, and stages keys t + 1 and values t
+    // (loaded a turn before, their pages looked up two before) into the buffers
+    // that turn t - 1 was the last to read.  Past the last tile nothing is
+    // loaded and what is staged is not read.
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[n][i] = 0.f;
+    for (int i = 0; i < 4; ++i) put_k(0, i);
+    {
+      const auto load = fetch(1, kpg_next, 0, 0);
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d)
+      for (int i = 0; i < 4; ++i) load(i);
+    }
+    kpg_next = key_page(2, ka);
+    __syncthreads();
+    float keep;
+    if (!whole_tile(0)) clean_v(0, vpg);
+    score_and_stage(0);
+    {
+      const auto load = fetch(2, kpg_next, 1, vpg_next);
 #pragma unroll
-          for (int n = 0; n < NS; ++n) {
-            const u32x4_t a = *(const u32x4_t *)(buf + (2 * d + h) * G::K_PIECE + (32 * n + col) * 16);
-            s[n] = mfma32<BF16>(a, q[d], s[n]);
-          }
-        // ---- mask: element 8t + 4u + i of product n is key k0 + 32n + 16t + 8h + 4u + i
-        const bool whole = k0 >= w_lo && k0 + BN <= w_hi && !holes;
-        auto sees = [&](int n, int i) __attribute__((always_inline)) {
-          return (uint32_t)(k0 + 32 * n + 16 * (i >> 3) + 8 * h + (i & 7) - first) < (uint32_t)span;
-        };
-        auto hole = [&](int n, int t8) __attribute__((always_inline)) {
-          return PAGED && holes && page_of(k0 + 32 * n + 16 * t8 + 8 * h) < 0;
-        };
-        if (!whole) {
+      for (int i = 0; i < 12; ++i) load(i);
+    }
+    vpg = vpg_next;
+    kpg_next = key_page(3, ka), vpg_next = key_page(2, va);
+    settle(0, keep);
+    weigh();
+    __syncthreads();
+    for (int t = 1; t < n_tiles; ++t) {
+      if (!whole_tile(t)) clean_v(t, vpg);
+      score_and_stage(t);
+      int grew = __builtin_amdgcn_readfirstlane((int)settle(t, keep));
+      asm volatile("" : "+s"(grew));  // one block of products and vector work for both cases
+      product_and_weigh(t - 1, fetch(t + 2, kpg_next, t + 1, vpg_next));
+      vpg = vpg_next;
+      kpg_next = key_page(t + 3, ka), vpg_next = key_page(t + 2, va);
+      if (grew) {
 #pragma unroll
-          for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int t8 = 0; t8 < 2; ++t8) {
-              const bool none = hole(n, t8);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const bool ok = sees(n, 8 * t8 + i) & !none;
-                s[n][8 * t8 + i] = ok ? s[n][8 * t8 + i] : -INFINITY;
-              }
-            }
-        }
-        // ---- the running maximum; o is scaled only when some row's grew by
-        // more than 2^8, so probabilities reach at most 2^8 (exact in range for
-        // both types, and the sums are fp32)
-        float top = s[0][0];
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[n][i]);
-        top = pair_max(top) * p.scale_log2;
-        if (__any(top > m + 8.f)) {
-          const float grown = __builtin_fmaxf(m, top);
-          const float keep = grown == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - grown);
-          m = grown;
-          l *= keep;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] *= keep;
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        // ---- probabilities
-        u32x4_t pr[NS][2];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-          for (int t8 = 0; t8 < 2; ++t8) {
-            float e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][8 * t8 + i], p.scale_log2, -base));
-              sum[i & 3] += e[i];
-            }
-            // rounded to the type for the product; the sum takes them unrounded
-#pragma unroll
-            for (int y = 0; y < 4; ++y) pr[n][t8][y] = Half<BF16>::pack(e[2 * y], e[2 * y + 1]);
-          }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // ---- values
-        const uint8_t *vb = buf + G::K_BYTES + col * 16;
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-          for (int t8 = 0; t8 < 2; ++t8)
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              const u32x4_t a = *(const u32x4_t *)(vb + ((4 * n + 2 * t8 + h) * D + 32 * d) * 16);
-              o[d] = mfma32<BF16>(a, pr[n][t8], o[d]);
-            }
+        for (int d = 0; d < DT; ++d) o[d] *= keep;
       }
       __syncthreads();
     }
+    product(n_tiles - 1);
   }
   l = pair_sum(l);
 
@@ -350,16 +464,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
       for (int key = max(k0, lo); key < min(k0 + BN, hi); ++key) {
         const int pg = PAGED ? page_of(key) : 0;
         if (pg < 0) continue;
-        const bool mine = (uint32_t)(key - first) < (uint32_t)span;
-        const int64_t row = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
+        const int64_t slot = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           const int piece = piece_of(x);
           uint32_t word[PW];
           float scale = 1.f;
           if constexpr (PAGED) {
-            load_words(word, p.cache.v + pg * p.cache.v_page + row * (D * CB / 8) + piece * CB);
-            if constexpr (CB < 16) scale = scale_of(p.cache.v_scale[pg * p.cache.vs_page + row * (D / 32) + (piece >> 2)]);
+            load_words(word, p.cache.v + pg * p.cache.v_page + slot * (D * CB / 8) + piece * CB);
+            if constexpr (CB < 16) scale = scale_of(p.cache.v_scale[pg * p.cache.vs_page + slot * (D / 32) + (piece >> 2)]);
           } else {
             load_words(word, (const uint8_t *)(p.v.data + (int64_t)(w.q0 + key) * p.v.token + (int64_t)head * p.v.head + 8 * piece));
           }
@@ -367,27 +480,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float f = Half<BF16>::up((v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
-            o[prod(j)][elem(x, j)] += mine && !__builtin_isfinite(f) ? f : 0.f;
+            o[prod(j)][elem(x, j)] += (uint32_t)(key - first) < (uint32_t)span && !__builtin_isfinite(f) ? f : 0.f;
           }
         }
       }
     }
   }
-  auto store_rows = [&]() __attribute__((always_inline)) {
-    if (!live) return;
-#pragma unroll
-    for (int x = 0; x < D / 16; ++x) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = o[prod(j)][elem(x, j)];
-      store_row<BF16, 8>(p, w, r, head, 8 * piece_of(x), v, l);
-    }
-  };
   if (w.splits > 1) {
-    // a part: [wave][o register / 4][lane][4], then m and the sum of each row
+    // a part: [wave][o register / 4][lane][4], then m and the sum of each row;
+    // waves whose rows the tile does not have neither write nor read
     constexpr int PART = R * (D + 2);
     constexpr int OV = 4 * DT;
-    const bool any = r0 + 32 * wave < rows;  // the wave has rows
+    const bool any = r0 + 32 * wave < rows;
     auto part_of = [&](int x) __attribute__((always_inline)) {
       return __builtin_amdgcn_make_buffer_rsrc(p.part + ((int64_t)(w.part - w.split + x) * p.heads_kv + head) * PART,
                                                (short)0, PART * 4, 0x00020000);
@@ -415,18 +519,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
       if (!any) return;
-      auto row_of = [&](int x, int which) __attribute__((always_inline)) {
-        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_of(x0 + x * step), (R * D + which * R + 32 * wave + col) * 4,
-                                                                    0, ATTN_CPOL_SC1));
+      auto of_row = [&](int x, int which) __attribute__((always_inline)) {
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            part_of(x0 + x * step), (R * D + which * R + 32 * wave + col) * 4, 0, ATTN_CPOL_SC1));
       };
 #pragma unroll 4
-      for (int x = 0; x < count; ++x) m = __builtin_fmaxf(m, row_of(x, 0));
+      for (int x = 0; x < count; ++x) m = __builtin_fmaxf(m, of_row(x, 0));
       const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
       for (int x = 0; x < count; ++x) {
         const auto rs = part_of(x0 + x * step);
-        const float f = __builtin_amdgcn_exp2f(row_of(x, 0) - base);
-        l += f * row_of(x, 1);
+        const float f = __builtin_amdgcn_exp2f(of_row(x, 0) - base);
+        l += f * of_row(x, 1);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -441,7 +545,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     put(w.split);
     if (!add_parts(p, w, head, add, put)) return;
   }
-  store_rows();
+  if (!live) return;
+#pragma unroll
+  for (int x = 0; x < D / 16; ++x) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = o[prod(j)][elem(x, j)];
+    store_row<BF16, 8>(p, w, row, head, 8 * piece_of(x), v, l);
+  }
 }
 
 }  // namespace exl3
