@@ -30,7 +30,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _BF16, _F16, _check, _HERE, _stream, _workspace, load
+from . import _BF16, _F16, _HERE, _check, _workspace, _workspaces, _ws_needs_zero, load
 
 __all__ = ["Rope", "KvCache", "split_heads", "rope", "cache_write", "cache_read", "rope_cache_write",
            "paged_attention", "prompt_attention", "attention_workspace_bytes"]
@@ -89,31 +89,52 @@ def attn_header_symbols() -> Tuple[str, ...]:
     return tuple(sorted(set(re.findall(r"\b(exl3_[a-z_]+)\s*\(", text))))
 
 
+_DTYPES = {torch.bfloat16: _BF16, torch.float16: _F16}
+
+
 def _dtype_id(dtype: torch.dtype, name: str) -> int:
-    if dtype == torch.bfloat16:
-        return _BF16
-    if dtype == torch.float16:
-        return _F16
-    raise ValueError(f"{name} has dtype {dtype}, expected bfloat16 or float16")
+    i = _DTYPES.get(dtype)
+    if i is None:
+        raise ValueError(f"{name} has dtype {dtype}, expected bfloat16 or float16")
+    return i
+
+
+# A call of a few microseconds on the GPU should not take three times as long
+# here: the current stream's handle straight from torch's binding (0.1 us; by
+# way of a Stream object 2.7 us), outputs by empty_like (1.0 us; torch.empty
+# with a shape, dtype and device 2.0 us), the workspace's lock only when there
+# is something to do.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _scratch(nbytes: int, device: torch.device, stream: int) -> Tuple[Optional[int], int]:
+    if nbytes == 0:
+        return None, 0
+    key = (device.index, stream)
+    ws = _workspaces.get(key)
+    if ws is not None and ws.numel() >= nbytes and key not in _ws_needs_zero:
+        return ws.data_ptr(), ws.numel()
+    return _workspace(nbytes, device)
 
 
 def _rows(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> _Rows:
     """The view of a [tokens, heads, head_dim] tensor, checked against `like`'s tokens, dtype and device."""
-    if t.dim() != 3 or t.shape[2] not in HEAD_DIMS:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, heads, 64, 128 or 256]")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] not in HEAD_DIMS:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens, heads, 64, 128 or 256]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if like is not None:
+    if like is not None and like is not t:
         if t.dtype != like.dtype or t.device != like.device:
             raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-        if t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {like.shape[0]} tokens of "
+        if shape[0] != like.shape[0] or shape[2] != like.shape[2]:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected {like.shape[0]} tokens of "
                              f"{like.shape[2]}-value heads")
-    st = t.stride()
-    if st[2] != 1:
-        raise ValueError(f"{name} has stride {st[2]} in its last dimension, expected 1")
+    tokens, heads, last = t.stride()
+    if last != 1:
+        raise ValueError(f"{name} has stride {last} in its last dimension, expected 1")
     # the stride of a dimension of one is never used and may be anything
-    return _Rows(t.data_ptr(), st[0] if t.shape[0] > 1 else 0, st[1] if t.shape[1] > 1 else 0, t.shape[1])
+    return _Rows(t.data_ptr(), tokens if shape[0] > 1 else 0, heads if shape[1] > 1 else 0, shape[1])
 
 
 def _ints(t: torch.Tensor, name: str, n: int, device) -> int:
@@ -125,7 +146,7 @@ def _ints(t: torch.Tensor, name: str, n: int, device) -> int:
 
 def _out(out: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tensor:
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     if out.shape != like.shape:
         raise ValueError(f"{name} has shape {tuple(out.shape)}, expected {tuple(like.shape)}")
     return out
@@ -274,7 +295,7 @@ def rope(r: Rope, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Te
     elif k_out is not None:
         raise ValueError("k_out without k")
     _check(_lib().exl3_rope(r._ref, _ints(positions, "positions", T, q.device), T, D, _dtype_id(q.dtype, "q"),
-                            ctypes.byref(qr), ctypes.byref(qo), kr, ko, _stream()))
+                            ctypes.byref(qr), ctypes.byref(qo), kr, ko, _raw_stream(q.device.index)))
     return q_out if k is None else (q_out, k_out)
 
 
@@ -292,7 +313,7 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
     if v.shape[0] != T:
         raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
     _check(_lib().exl3_cache_write(cache._ref, ctypes.byref(kr), ctypes.byref(vr),
-                                   _ints(slots, "slots", T, cache.device), T, _stream()))
+                                   _ints(slots, "slots", T, cache.device), T, _raw_stream(cache.device.index)))
 
 
 def rope_cache_write(cache: KvCache, r: Rope, positions: torch.Tensor, slots: torch.Tensor, q: torch.Tensor,
@@ -309,7 +330,7 @@ def rope_cache_write(cache: KvCache, r: Rope, positions: torch.Tensor, slots: to
     ko = ctypes.byref(_rows(_out(k_out, k, "k_out"), "k_out", k)) if k_out is not None else None
     _check(_lib().exl3_rope_cache_write(cache._ref, r._ref, _ints(positions, "positions", T, q.device),
                                         _ints(slots, "slots", T, q.device), T, ctypes.byref(qr), ctypes.byref(qo),
-                                        ctypes.byref(kr), ko, ctypes.byref(vr), _stream()))
+                                        ctypes.byref(kr), ko, ctypes.byref(vr), _raw_stream(cache.device.index)))
     return q_out
 
 
@@ -319,14 +340,14 @@ def cache_read(cache: KvCache, slots: torch.Tensor, k_out: Optional[torch.Tensor
     n = slots.shape[0]
     shape = (n, cache.heads, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        k_out = slots.new_empty(shape, dtype=cache.dtype)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        v_out = torch.empty_like(k_out, memory_format=torch.contiguous_format)
     kr, vr = _cache_rows(cache, k_out, "k_out"), _cache_rows(cache, v_out, "v_out")
     if k_out.shape[0] != n or v_out.shape[0] != n:
         raise ValueError(f"{n} slots, k_out has {k_out.shape[0]} tokens, v_out {v_out.shape[0]}")
     _check(_lib().exl3_cache_read(cache._ref, _ints(slots, "slots", n, cache.device), n, ctypes.byref(kr),
-                                  ctypes.byref(vr), _stream()))
+                                  ctypes.byref(vr), _raw_stream(cache.device.index)))
     return k_out, v_out
 
 
@@ -360,11 +381,11 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
     o = _rows(out, "out", q)
     L = _lib()
     need = L.exl3_attention_workspace_bytes(B, T, H, cache.heads, D)
-    ws, wsn = _workspace(need, dev) if need else (None, 0)
+    stream = _raw_stream(dev.index)
+    ws, wsn = _scratch(need, dev, stream)
     _check(L.exl3_paged_attention(cache._ref, ctypes.byref(qr), ctypes.byref(o), _ints(cu_q, "cu_q", B + 1, dev),
                                   _ints(kv_len, "kv_len", B, dev), page_table.data_ptr(), page_table.stride(0),
-                                  page_table.shape[1], B, T, D ** -0.5 if scale is None else scale, window, ws, wsn,
-                                  _stream()))
+                                  page_table.shape[1], B, T, D ** -0.5 if scale is None else scale, window, ws, wsn, stream))
     return out
 
 
@@ -380,8 +401,9 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     o = _rows(out, "out", q)
     L = _lib()
     need = L.exl3_attention_workspace_bytes(B, T, H, k.shape[1], D)
-    ws, wsn = _workspace(need, q.device) if need else (None, 0)
+    stream = _raw_stream(q.device.index)
+    ws, wsn = _scratch(need, q.device, stream)
     _check(L.exl3_prompt_attention(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(o),
                                    _ints(cu_seqlens, "cu_seqlens", B + 1, q.device), B, T, D, _dtype_id(q.dtype, "q"),
-                                   int(causal), window, D ** -0.5 if scale is None else scale, ws, wsn, _stream()))
+                                   int(causal), window, D ** -0.5 if scale is None else scale, ws, wsn, stream))
     return out
