@@ -109,7 +109,7 @@ exl3_status exl3_cache_read(const exl3_kv_cache *c, const int32_t *slots, int32_
  * cu_q[s] .. cu_q[s+1]-1 (int32 [batch+1], non-decreasing, from 0 to tokens)
  * and kv_len[s] keys (int32 [batch]), the new tokens' own among them: its i-th
  * query stands at position p = kv_len - q_len + i and sees the keys 0..p, or
- * p-window+1..p when window > 0.  Key j is at offset j % page_size of page
+ * p-window+1..p when window > 0 (at most 2^30).  Key j is at offset j % page_size of page
  * page_table[s][j / page_size] (int32, row stride page_table_stride, width
  * page_table_width); a page outside 0..pages-1, or past the width, is a hole
  * whose keys nobody sees.  Query head h reads the cache's head
@@ -124,7 +124,8 @@ exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, con
 /* Attention within packed sequences: sequence s is the rows cu[s]..cu[s+1]-1
  * of q, k and v (int32 [batch+1], as cu_q above).  causal: row i sees 0..i of
  * its sequence, else all of it; window > 0 (causal only) the last `window` of
- * those.  k and v have the same heads, q a multiple of them. */
+ * those.  k and v have the same heads, q a multiple of them, and token strides
+ * of at most 2^22 (the kernels address a tile of keys by 32-bit offsets). */
 exl3_status exl3_prompt_attention(const exl3_rows *q, const exl3_rows *k, const exl3_rows *v, const exl3_rows *out,
                                   const int32_t *cu, int32_t batch, int32_t tokens, int32_t head_dim, int32_t dtype,
                                   int32_t causal, int32_t window, float scale, void *workspace, size_t workspace_bytes,

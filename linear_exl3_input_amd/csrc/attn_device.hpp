@@ -55,6 +55,10 @@ struct Half<false> {
   }
 };
 
+__device__ __forceinline__ int quotient(int n, const Divisor &d) {
+  return d.mul == 0u ? n : (int)(__umulhi((uint32_t)n, d.mul) >> d.shift);
+}
+
 // ------------------------------------------------------- codes and scales
 
 // The scale of byte s as a float: 2^(s - 127).  255, a block that held a NaN
@@ -143,7 +147,8 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       x.kv = p.kv_len ? max(0, p.kv_len[s]) : x.ql;
       x.tiles = (int)(((int64_t)x.ql * p.group + R - 1) / R);
       // a tile's rows are at most R tokens; its keys start at a multiple of 32
-      x.span = p.window > 0 ? min(x.kv, min(p.window, 0x3FFFFFFF) + R + 32) : x.kv;
+      x.span = p.kv_len ? min(x.kv, p.table_keys) : x.kv;
+      if (p.window > 0) x.span = min(x.span, p.window + R + 32);
     }
     return x;
   };
@@ -193,7 +198,9 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       w.q_len = __builtin_amdgcn_readlane(x.ql, l);
       w.kv_len = __builtin_amdgcn_readlane(x.kv, l);
       w.part = w.splits > 1 ? pbase + __builtin_amdgcn_readlane(pincl - parts, l) + at : 0;
-      return true;
+      // (more parts than there is room for can only come from sequences that
+      // overlap; such tiles are left out)
+      return w.splits == 1 || w.part - w.split + w.splits <= p.part_cap;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
     pbase += __builtin_amdgcn_readlane(pincl, 63);
@@ -212,13 +219,14 @@ struct KeyRange {
 __device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w, int r0, int r_last) {
   KeyRange k;
   k.shift = w.kv_len - w.q_len;
-  k.p_first = k.shift + r0 / p.group;
-  k.p_last = k.shift + r_last / p.group;
+  k.p_first = k.shift + quotient(r0, p.by_group);
+  k.p_last = k.shift + quotient(r_last, p.by_group);
   k.hi = p.causal ? min(w.kv_len, k.p_last + 1) : w.kv_len;
+  if (p.kv_len) k.hi = min(k.hi, p.table_keys);  // past the table everything is a hole
   k.lo = p.window > 0 ? max(0, k.p_first - p.window + 1) : 0;
   if (w.splits > 1) {
     const int64_t from = (int64_t)(k.lo & ~31) + (int64_t)w.split * w.part_keys;
-    k.lo = (int)min<int64_t>(max<int64_t>(from, k.lo), 0x7FFFFF00);
+    k.lo = (int)min<int64_t>(max<int64_t>(from, k.lo), MAX_KEYS);
     k.hi = (int)min<int64_t>(from + w.part_keys, k.hi);
   }
   k.start = k.lo & ~31;

@@ -15,6 +15,7 @@ using exl3::host_fail;
 constexpr int32_t MAX_TOKENS = 1 << 20;
 constexpr int32_t MAX_HEADS = 1024;
 constexpr int32_t MAX_BATCH = 1 << 16;
+constexpr int32_t MAX_WINDOW = 1 << 30;  // a position minus a window fits 32 bits
 constexpr int64_t MAX_GRID = 0x7FFFFFFF;
 
 exl3_status check_ptr(const void *p, const char *name) {
@@ -162,7 +163,7 @@ exl3_status launched(hipError_t e, const char *what) {
 struct AttnPlan {
   int32_t columns;  // 16-row column tiles of a workgroup of the small kernel; 0: the tile kernel
   int32_t target;   // work items per head that splitting aims at; 0: keys are not split
-  int32_t part_min;
+  int32_t part_min, part_cap;
   size_t workspace;
 };
 
@@ -173,9 +174,29 @@ struct AttnPlan {
 // even out (64 sequences of up to 16000 keys, 8 bits: 242 us in one round, 190
 // in two, 201 in four; chunks of up to 1000 tokens over 20000 keys on the tile
 // kernel: 890, 803 and 712 us in one, two and four).
-constexpr int32_t PART_MIN = 256;  // least keys of a part
-// A sequence's rows on one key/value head from which the tile kernel runs.
-constexpr double TILE_MIN_ROWS = 64.0;
+//
+// The least keys of a part: splitting costs the write and the read of a part's
+// sums, 8 KB (heads of 128) in the small kernel, 66 KB in the tile kernel (132
+// KB with heads of 256).  One token over 1100 keys takes 10.3 us in parts of 128
+// keys at least, 9.4 in parts of 256, 10.7 in parts of 384 and 12.2 in parts of
+// 1024.  On the tile kernel prompts of up to 300 tokens take 23 us split in two
+// and 14 us whole, 16 sequences of 8 tokens over 4000 keys (24/4 heads of 256)
+// 347 us in parts of 256 and 100 in parts of 1024, 16 of 16 tokens (32/8 heads
+// of 128) 74 us in parts of 512 and 57 in parts of 1024.
+constexpr int32_t PART_MIN = 256;
+constexpr int32_t TILE_PART_MIN = 1024;
+
+// A sequence's rows on one key/value head above which the tile kernel runs.
+// Measured small / tile: heads of 64, 16 sequences of 4000 keys, 64 rows 43 /
+// 37 us; heads of 128, 32 rows 51 / 53, 64 rows 61 / 57 (one sequence of 30000
+// keys 39 / 43), 96 rows 87 / 62 (61 / 43); heads of 256, 48 rows 118 / 100, 96
+// rows 167 / 104, but two sequences of 30000 keys, 96 rows, 87 / 171: few tiles
+// of them need many parts, whose sums are large.
+double tile_min_rows(int32_t batch, int32_t kv_heads, int32_t head_dim) {
+  if (head_dim == 64) return 48.0;
+  if (head_dim == 128) return 64.0;
+  return 8 * (int64_t)batch * kv_heads <= exl3::host_cus() ? 128.0 : 32.0;
+}
 
 exl3_status check_attention_sizes(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads) {
   if (batch < 0 || batch > MAX_BATCH)
@@ -191,21 +212,23 @@ exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads, int32
                            AttnPlan *pl) {
   const int32_t group = q_heads / kv_heads;
   const double rows = batch > 0 ? (double)tokens * group / batch : 0.0;  // a sequence's, on one key/value head
-  pl->columns = rows > TILE_MIN_ROWS ? 0 : rows > 32.0 && head_dim == 64 ? 4 : rows > 16.0 && head_dim < 256 ? 2 : 1;
+  pl->columns = rows > tile_min_rows(batch, kv_heads, head_dim) ? 0 : rows > 16.0 && head_dim < 256 ? 2 : 1;
   pl->target = 0;
-  pl->part_min = PART_MIN;
   pl->workspace = 0;
   const bool tile = pl->columns == 0;
+  pl->part_min = tile ? TILE_PART_MIN : PART_MIN;
   const int32_t R = tile ? exl3::ATTN_TILE_ROWS : 16 * pl->columns;
   const int64_t tiles = (int64_t)tokens * group / R + batch;  // at most, on each key/value head
   const int64_t per_cu = (tile ? head_dim == 256 : head_dim * pl->columns >= 256) ? 1 : 2;  // workgroups, by registers
   const int64_t round = per_cu * exl3::host_cus();
   const int64_t rounds = 4 * tiles * kv_heads <= round ? 1 : tile ? 4 : 2;
   const int64_t want = std::max<int64_t>(kv_heads, rounds * round);
-  if (tiles * kv_heads < want) {
+  pl->part_cap = 0;
+  const int64_t parts = std::min(2 * (want / kv_heads), want / kv_heads + tiles);
+  if (tiles * kv_heads < want && parts * kv_heads <= EXL3_WORKSPACE_COUNTER_BYTES / 4) {
     pl->target = (int32_t)(want / kv_heads);
-    pl->workspace = EXL3_WORKSPACE_COUNTER_BYTES + (size_t)std::min(2 * (int64_t)pl->target, pl->target + tiles) *
-                                                       kv_heads * R * (head_dim + 2) * sizeof(float);
+    pl->part_cap = (int32_t)parts;
+    pl->workspace = EXL3_WORKSPACE_COUNTER_BYTES + (size_t)parts * kv_heads * R * (head_dim + 2) * sizeof(float);
   }
   const int64_t items = tiles + pl->target;
   if (items * kv_heads > MAX_GRID)
@@ -228,6 +251,7 @@ exl3_status run_attention(exl3::AttnParams &p, int32_t head_dim, bool bf16, int3
   }
   p.target = pl.target;
   p.part_min = pl.part_min;
+  p.part_cap = pl.part_cap;
   const hipError_t e = pl.columns > 0 ? exl3::launch_attn_small(head_dim, bf16, bits, p, pl.columns, s)
                                       : exl3::launch_attn_tile(head_dim, bf16, bits, p, s);
   return launched(e, "attention launch");
@@ -428,7 +452,8 @@ exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, con
   if (page_table_width < 0 || page_table_stride < 0)
     return host_fail(EXL3_ERR_INVALID_ARG, "page table width=%d stride=%lld are negative", page_table_width,
                      (long long)page_table_stride);
-  if (window < 0) return host_fail(EXL3_ERR_INVALID_ARG, "window=%d is negative", window);
+  if (window < 0 || window > MAX_WINDOW)
+    return host_fail(EXL3_ERR_INVALID_ARG, "window=%d, must be 0 (none) to %d", window, MAX_WINDOW);
   if ((st = check_scale(scale)) != EXL3_OK) return st;
   if (tokens == 0) return EXL3_OK;
   if (batch == 0) return host_fail(EXL3_ERR_INVALID_ARG, "batch=0 with %d tokens", tokens);
@@ -445,10 +470,12 @@ exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, con
   p.page_table = page_table;
   p.table_stride = page_table_stride;
   p.table_width = page_table_width;
+  p.table_keys = (int32_t)std::min<int64_t>((int64_t)page_table_width * c->page_size, exl3::MAX_KEYS);
   p.batch = batch;
   p.tokens = tokens;
   p.heads_kv = c->heads;
   p.group = q->heads / c->heads;
+  p.by_group = exl3::Divisor::of((uint32_t)p.group);
   p.causal = 1;
   p.window = window;
   p.scale_log2 = scale * LOG2E;
@@ -477,8 +504,9 @@ exl3_status exl3_prompt_attention(const exl3_rows *q, const exl3_rows *k, const 
   if (k->heads != v->heads) return host_fail(EXL3_ERR_INVALID_ARG, "k has %d heads, v %d", k->heads, v->heads);
   if ((st = check_attention_sizes(batch, tokens, q->heads, k->heads)) != EXL3_OK) return st;
   if (causal != 0 && causal != 1) return host_fail(EXL3_ERR_INVALID_ARG, "causal=%d, must be 0 or 1", causal);
-  if (window < 0 || (window > 0 && !causal))
-    return host_fail(EXL3_ERR_INVALID_ARG, "window=%d with causal=%d: a window is positive and causal", window, causal);
+  if (window < 0 || window > MAX_WINDOW || (window > 0 && !causal))
+    return host_fail(EXL3_ERR_INVALID_ARG, "window=%d with causal=%d: 0 (none) to %d, and a window is causal", window,
+                     causal, MAX_WINDOW);
   if ((st = check_scale(scale)) != EXL3_OK) return st;
   if (tokens == 0) return EXL3_OK;
   if (batch == 0) return host_fail(EXL3_ERR_INVALID_ARG, "batch=0 with %d tokens", tokens);
@@ -494,6 +522,7 @@ exl3_status exl3_prompt_attention(const exl3_rows *q, const exl3_rows *k, const 
   p.tokens = tokens;
   p.heads_kv = k->heads;
   p.group = q->heads / k->heads;
+  p.by_group = exl3::Divisor::of((uint32_t)p.group);
   p.causal = causal;
   p.window = window;
   p.scale_log2 = scale * LOG2E;

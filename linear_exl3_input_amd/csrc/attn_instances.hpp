@@ -55,9 +55,6 @@ hipError_t EXL3_JOIN(launch_attn_small_d, EXL3_HEAD_DIM)(bool bf16, int bits, co
 #if EXL3_HEAD_DIM < 256  // two column tiles of 256-value heads do not fit the registers
   if (columns == 2) return bf16 ? small_bits<true, 2>(bits, p, s) : small_bits<false, 2>(bits, p, s);
 #endif
-#if EXL3_HEAD_DIM == 64
-  if (columns == 4) return bf16 ? small_bits<true, 4>(bits, p, s) : small_bits<false, 4>(bits, p, s);
-#endif
   if (columns != 1) return hipErrorInvalidValue;
   return bf16 ? small_bits<true, 1>(bits, p, s) : small_bits<false, 1>(bits, p, s);
 }

@@ -66,10 +66,9 @@ __global__ __launch_bounds__(256) void rows_kernel(RowsParams p) {
   const int c = threadIdx.x % LPR;
   const int64_t row = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
   const int H = p.hq + p.hk + p.hv;
-  // rows number at most 2^20 tokens of 3 * 1024 heads
+  if (row >= (int64_t)p.tokens * H) return;  // whole rows leave: the quads below stay full
   const uint32_t t = (uint32_t)row / (uint32_t)H;
   int h = (int)((uint32_t)row - t * (uint32_t)H);
-  if (row >= (int64_t)p.tokens * H) return;  // whole rows leave: the quads below stay full
   const bool is_q = h < p.hq, is_v = h >= p.hq + p.hk;
   const Rows src = is_q ? p.q : is_v ? p.v : p.k;
   h -= is_q ? 0 : is_v ? p.hq + p.hk : p.hq;

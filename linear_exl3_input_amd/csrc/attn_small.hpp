@@ -104,12 +104,26 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
   return x;
 }
 
+// The largest (the sum) of the four lanes that hold a column, 16 lanes apart.
+__device__ __forceinline__ float column_max(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // N consecutive dims, from d on, of row r of the tile's sequence.
 template <bool BF16, int N>
 __device__ __forceinline__ void store_row(const AttnParams &p, const Work &w, int r, int head, int d,
                                           const float (&v)[N], float total) {
   const float inv = total == 0.f ? 0.f : 1.f / total;  // a row that sees no key is zero
-  const int i = r / p.group, h = r - i * p.group;
+  const int i = quotient(r, p.by_group), h = r - i * p.group;
   uint16_t *y = p.out.data + (int64_t)(w.q0 + i) * p.out.token + (int64_t)(head * p.group + h) * p.out.head + d;
   uint32_t x[N / 2];
 #pragma unroll
@@ -131,7 +145,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   constexpr int DP = D / 32;             // as pairs
   using KR = KeyRun<D, CB>;
   constexpr int VW = DV * CB >= 32 ? DV * CB / 32 : 1;  // words of a lane's dims of one value row
-  __shared__ float s_o[4][64][DV + 1];
+  __shared__ float s_o[4][4][64][DV + 1];  // [element i][wave][lane][operand j]
   __shared__ float s_m[4][R], s_l[4][R];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -148,6 +162,27 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   const KeyRange kr = key_range(p, w, r0, r_last);
   const int lo = kr.lo, hi = kr.hi, p_first = kr.p_first, p_last = kr.p_last, shift = kr.shift;
 
+  // ---- where keys and values lie
+  const int ps_mask = (1 << p.cache.page_shift) - 1;
+  const int32_t *table = PAGED ? p.page_table + (int64_t)w.seq * p.table_stride : nullptr;
+  // lane's keys of a step at k0: first product k0 + 8*(c/4) + c%4 and 4 more,
+  // second product k0 + 8*g .. + 7; each within one page (pages hold whole 16s)
+  auto page_of = [&](int key) __attribute__((always_inline)) -> int {
+    const int i = key >> p.cache.page_shift;
+    int pg = -1;
+    if (key < hi && i < p.table_width) pg = table[i];
+    return pg >= 0 && pg < p.cache.pages ? pg : -1;
+  };
+  // Pages are looked up two steps ahead: loads complete in order, so a step's
+  // rows must not wait for a page number issued after the step before's rows.
+  int k0 = kr.start + 32 * wave;
+  int pk = 0, pv = 0, pk2 = 0, pv2 = 0;  // pages of this step's and the next step's keys and values
+  if constexpr (PAGED) {
+    pk = page_of(k0 + 8 * (c >> 2));
+    pv = page_of(k0 + 8 * g);
+    pk2 = page_of(k0 + 128 + 8 * (c >> 2));
+    pv2 = page_of(k0 + 128 + 8 * g);
+  }
   int first[NT], span[NT];  // the keys first .. first + span - 1 are those the lane's row (column c of tile n) sees
   const uint16_t *q_row[NT];
   bool live[NT];
@@ -155,7 +190,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   for (int n = 0; n < NT; ++n) {
     const int r = r0 + 16 * n + c;
     live[n] = r < rows;
-    const int i = (live[n] ? r : r_last) / p.group;
+    const int i = quotient(live[n] ? r : r_last, p.by_group);
     const int h = (live[n] ? r : r_last) - i * p.group;
     const int pos = shift + i;
     first[n] = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
@@ -172,17 +207,6 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
       q[n][t] = *(const u32x4_t *)(q_row[n] + u * 4 * KR::LEN + g * KR::LEN + 8 * e);
     }
 
-  // ---- where keys and values lie
-  const int ps_mask = (1 << p.cache.page_shift) - 1;
-  const int32_t *table = PAGED ? p.page_table + (int64_t)w.seq * p.table_stride : nullptr;
-  // lane's keys of a step at k0: first product k0 + 8*(c/4) + c%4 and 4 more,
-  // second product k0 + 8*g .. + 7; each within one page (pages hold whole 16s)
-  auto page_of = [&](int key) __attribute__((always_inline)) -> int {
-    const int i = key >> p.cache.page_shift;
-    int pg = -1;
-    if (key < hi && i < p.table_width) pg = table[i];
-    return pg >= 0 && pg < p.cache.pages ? pg : -1;
-  };
   uint32_t kw[2][KR::LOADS][KR::WORDS], vw[8][VW];
   uint32_t ksc[2][2], vsc[8];  // scale bytes: of a key's row, of the lane's block of a value row
   auto load_k = [&](int k0, int pg) __attribute__((always_inline)) {
@@ -246,17 +270,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     for (int j = 0; j < DV; ++j) o[n][j] = (float4_t){0.f, 0.f, 0.f, 0.f};
   }
 
-  // Pages are looked up two steps ahead: loads complete in order, so a step's
-  // rows must not wait for a page number issued after the step before's rows.
-  int k0 = kr.start + 32 * wave;
-  int pk = 0, pv = 0, pk2 = 0, pv2 = 0;  // pages of this step's and the next step's keys and values
   if (k0 < hi) {
-    if constexpr (PAGED) {
-      pk = page_of(k0 + 8 * (c >> 2));
-      pv = page_of(k0 + 8 * g);
-      pk2 = page_of(k0 + 128 + 8 * (c >> 2));
-      pv2 = page_of(k0 + 128 + 8 * g);
-    }
     load_k(k0, pk);
     load_v(k0, pv);
   }
@@ -312,16 +326,24 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     u32x4_t pr[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float top = m[n];
+      float top = s[n][0][0];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[n][t][i]);
-      top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-      const float base = top == -INFINITY ? 0.f : top;
-      const float keep = __builtin_amdgcn_exp2f(m[n] - base);
-      m[n] = top;
+      top = column_max(top);
+      // The running maximum moves, and o is scaled, only when some row's grew by
+      // more than 2^8: probabilities reach at most 2^8, within range for both
+      // types, and the sums are fp32.
+      if (__any(top > m[n] + 8.f)) {
+        const float grown = __builtin_fmaxf(m[n], top);
+        const float keep = grown == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[n] - grown);
+        m[n] = grown;
+        l[n] *= keep;
+#pragma unroll
+        for (int j = 0; j < DV; ++j) o[n][j] *= keep;
+      }
+      const float base = m[n] == -INFINITY ? 0.f : m[n];
       float pf[8];
       float sum = 0.f;
 #pragma unroll
@@ -331,9 +353,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
           pf[4 * t + i] = __builtin_amdgcn_exp2f(s[n][t][i] - base);
           sum += pf[4 * t + i];
         }
-      l[n] = l[n] * keep + sum;
-#pragma unroll
-      for (int j = 0; j < DV; ++j) o[n][j] *= keep;
+      l[n] += sum;
       // rounded to the type for the product (error 2^-9 or 2^-12 of each
       // term, no larger than the output's own rounding); l sums them unrounded
       pr[n] = (u32x4_t){Half<BF16>::pack(pf[0], pf[1]), Half<BF16>::pack(pf[2], pf[3]), Half<BF16>::pack(pf[4], pf[5]),
@@ -425,8 +445,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   // ---- the waves' results together: wave i sums element i of every tile
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    l[n] += __shfl_xor(l[n], 16, 64);
-    l[n] += __shfl_xor(l[n], 32, 64);
+    l[n] = column_sum(l[n]);
     if (g == 0) {
       s_m[wave][16 * n + c] = m[n];
       s_l[wave][16 * n + c] = l[n];
@@ -445,17 +464,15 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 #pragma unroll
     for (int x = 0; x < 4; ++x) total[n] += s_l[x][16 * n + c] * __builtin_amdgcn_exp2f(s_m[x][16 * n + c] - base);
     const float keep = __builtin_amdgcn_exp2f(m[n] - base);
-    for (int i = 0; i < 4; ++i) {
-      __syncthreads();
+    if (n > 0) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < DV; ++j)
-        s_o[wave][lane][j] = (i == 0 ? o[n][j][0] : i == 1 ? o[n][j][1] : i == 2 ? o[n][j][2] : o[n][j][3]) * keep;
-      __syncthreads();
-      if (wave == i) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < DV; ++j) mine[n][j] = (s_o[0][lane][j] + s_o[1][lane][j]) + (s_o[2][lane][j] + s_o[3][lane][j]);
-      }
-    }
+      for (int j = 0; j < DV; ++j) s_o[i][wave][lane][j] = o[n][j][i] * keep;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < DV; ++j)
+      mine[n][j] = (s_o[wave][0][lane][j] + s_o[wave][1][lane][j]) + (s_o[wave][2][lane][j] + s_o[wave][3][lane][j]);
   }
   if (w.splits > 1) {
     // a part: o as [n][wave][lane][DV], then m and the sum of each row; rows

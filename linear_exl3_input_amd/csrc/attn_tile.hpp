@@ -98,14 +98,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // ---- the lane's row, which sees the keys first .. first + span - 1
   const int row = r0 + 32 * wave + col;
   const bool live = row < rows;
-  const int tok = (live ? row : r_last) / p.group;
+  const int tok = quotient(live ? row : r_last, p.by_group);
   const int qh = (live ? row : r_last) - tok * p.group;
   const int pos = shift + tok;
   const int first = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
   const int span = max(0, (p.causal ? min(hi, pos + 1) : hi) - first);
   // of the wave's rows, first to last, every one sees [w_lo, w_hi)
-  const int wp0 = shift + min(r0 + 32 * wave, r_last) / p.group;
-  const int wp1 = shift + min(r0 + 32 * wave + 31, r_last) / p.group;
+  const int wp0 = shift + quotient(min(r0 + 32 * wave, r_last), p.by_group);
+  const int wp1 = shift + quotient(min(r0 + 32 * wave + 31, r_last), p.by_group);
   const int w_hi = p.causal ? min(hi, wp0 + 1) : hi, w_lo = p.window > 0 ? max(lo, wp1 - p.window + 1) : lo;
   u32x4_t q[D / 16];
   {

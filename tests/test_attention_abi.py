@@ -176,13 +176,34 @@ def prompt(q=None, k=None, v=None, out=None, cu=FAKE, batch=2, tokens=5, d=128, 
 
 @pytest.mark.parametrize("kw,msg", [
     (dict(k=rows(3)), "k has 3 heads, v 2"), (dict(k=rows(3), v=rows(3)), "multiple of the 3"),
-    (dict(causal=2), "causal=2"), (dict(causal=0, window=4), "a window is positive and causal"), (dict(window=-1), "window=-1"),
+    (dict(causal=2), "causal=2"), (dict(causal=0, window=4), "a window is causal"), (dict(window=-1), "window=-1"),
     (dict(d=32), "head_dim=32"), (dict(cu=None), "cu is NULL"), (dict(batch=0), "batch=0"), (dict(dtype=3), "dtype=3"),
     (dict(v=rows(2, data=FAKE + 2)), "v="), (dict(scale=0.0), "scale=0"),
 ])
 def test_prompt_refusals(kw, msg):
     assert prompt(**kw) in (1, 2)
     assert msg in last()
+
+
+def test_windows_and_strides_past_32_bit_offsets_are_refused():
+    assert paged(window=(1 << 30) + 1) == 1 and "window=1073741825" in last()
+    assert prompt(window=(1 << 30) + 1) == 1 and "window=1073741825" in last()
+    wide = rows(2, token=(1 << 22) + 8)
+    assert prompt(k=wide) == 2 and "token strides of k (4194312)" in last()
+    assert prompt(v=wide) == 2 and "and v (4194312)" in last()
+
+
+def test_workspace_holds_counters_and_parts_and_is_needed_only_with_few_tiles():
+    """One token over one cache is split, so it needs the counters and partial sums; prompts whose tiles fill the
+    GPU four times over need nothing; a call with a shorter workspace than it needs is refused."""
+    need = ex.attention_workspace_bytes(1, 1, 32, 8, 128)
+    assert need > 65536 and (need - 65536) % (16 * 130 * 4) == 0
+    assert ex.attention_workspace_bytes(1, 100000, 32, 8, 128) == 0
+    assert ex.attention_workspace_bytes(0, 0, 32, 8, 128) >= 0
+    for short in (0, need - 16):
+        st = paged(q=rows(32), out=rows(32), c=cache(heads=8, bits=16, page=16, k_page_bytes=8 * 16 * 256, v_page_bytes=8 * 16 * 256),
+                   batch=1, tokens=1, ws=FAKE if short else None, n=short)
+        assert st == 3 and f"short by {need - short}" in last()
 
 
 def test_workspace_query_refusals():
