@@ -109,11 +109,13 @@ exl3_status exl3_cache_read(const exl3_kv_cache *c, const int32_t *slots, int32_
  * cu_q[s] .. cu_q[s+1]-1 (int32 [batch+1], non-decreasing, from 0 to tokens)
  * and kv_len[s] keys (int32 [batch]), the new tokens' own among them: its i-th
  * query stands at position p = kv_len - q_len + i and sees the keys 0..p, or
- * p-window+1..p when window > 0 (at most 2^30).  Key j is at offset j % page_size of page
- * page_table[s][j / page_size] (int32, row stride page_table_stride, width
- * page_table_width); a page outside 0..pages-1, or past the width, is a hole
- * whose keys nobody sees.  Query head h reads the cache's head
- * h / (q.heads / heads).  Rows that see no key are zero.
+ * p-window+1..p when window > 0 (at most 2^30).  Key j is at offset
+ * j % page_size of page page_table[s][j / page_size] (int32, row stride
+ * page_table_stride, width page_table_width); a page outside 0..pages-1, or
+ * past the width, is a hole whose keys nobody sees.  Query head h reads the
+ * cache's head h / (q.heads / heads).  Rows that see no key are zero.  A cu_q
+ * that is not as above leaves out's values undefined and may leave counters in
+ * the workspace that have to be cleared before its next use.
  *   out = softmax(scale * q k^T) v, products in the cache's dtype with fp32
  * sums, the probabilities rounded to that type for the second product. */
 exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out, const int32_t *cu_q,

