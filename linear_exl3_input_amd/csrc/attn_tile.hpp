@@ -28,21 +28,22 @@
 // staging beside them, then the products with the values of tile t - 1 with
 // the exponentials of tile t and the loads of tile t + 2 beside them, so that
 // matrix, vector and memory work go on together.  The order is written out
-// and held by scheduling barriers: left to the compiler the same turn took
-// 4% (prompts of 8000 tokens) to 15% (heads of 256) longer.
+// and held by scheduling barriers; with it, staging by every wave and the
+// products' results in VGPRs, windows with heads of 256 went from 403 to 283
+// us and prompts of up to 8000 tokens from 1004 to 982.
 //
-// What bounds it: LDS reads and vector work, each about as long as the
-// products.  A wave-tile is 32 products of 32x32x16 (1024 cycles of its
-// SIMD's matrix unit), 32 KB of LDS reads (32 rows a wave: four waves take
-// 1024 cycles of the CU's 128 bytes a cycle) and some 1060 cycles of vector
-// work, half of them exponentials.  Measured: prompts of up to 8000 tokens,
-// 32/8 heads of 128, 931 GFLOP in 960 us, 970 TFLOP/s (a large matrix product
-// reaches 1283 here); chunks of up to 1000 tokens over up to 20000 keys of 8
-// bits, 523 GFLOP in 670 us, 780; windows of 2048, 24/4 heads of 256, 206
-// GFLOP in 278 us, 743 (one wave a SIMD, as o alone takes 128 registers).
-// 64 rows a wave halve the LDS reads but spill; eight waves as two groups of
-// four that alternate products and vector work take 925 us on the first but
-// more on chunks, and spill with heads of 256.
+// What bounds it: vector work about as long as the products, on the same
+// SIMDs.  A wave-tile is 32 products of 32x32x16 (1024 cycles of its SIMD's
+// matrix unit), some 1060 cycles of vector work, half of them exponentials,
+// and 32 KB of LDS reads; counters show the matrix units busy for 48% of the
+// cycles, the vector units for 50%, the LDS for 36%.  Measured: prompts of up
+// to 8000 tokens, 32/8 heads of 128, 931 GFLOP in 960 us, 970 TFLOP/s (a large
+// matrix product reaches 1283 here); chunks of up to 1000 tokens over up to
+// 20000 keys of 8 bits, 523 GFLOP in 670 us, 780; windows of 2048, 24/4 heads
+// of 256, 206 GFLOP in 278 us, 743 (one wave a SIMD, as o alone takes 128
+// registers).  64 rows a wave halve the LDS reads but spill; eight waves as
+// two groups of four that alternate products and vector work take 925 us on
+// the first but more on chunks, and spill with heads of 256.
 #pragma once
 
 #include "attn_small.hpp"
