@@ -118,22 +118,40 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
 
   // ---- the lane's row, which sees the keys first .. first + span - 1
   const int row = r0 + 32 * wave + col;
-  const bool live = row < rows;
-  const int tok = quotient(live ? row : r_last, p.by_group);
-  const int qh = (live ? row : r_last) - tok * p.group;
-  const int pos = shift + tok;
+  const int pos = shift + quotient(min(row, r_last), p.by_group);
   const int first = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
   const int span = max(0, (p.causal ? min(hi, pos + 1) : hi) - first);
   // of the wave's rows, first to last, every one sees [w_lo, w_hi)
   const int wp0 = shift + quotient(min(r0 + 32 * wave, r_last), p.by_group);
   const int wp1 = shift + quotient(min(r0 + 32 * wave + 31, r_last), p.by_group);
   const int w_hi = p.causal ? min(hi, wp0 + 1) : hi, w_lo = p.window > 0 ? max(lo, wp1 - p.window + 1) : lo;
-  u32x4_t q[D / 16];
-  {
-    const uint16_t *a = p.q.data + (int64_t)(w.q0 + tok) * p.q.token + (int64_t)(head * p.group + qh) * p.q.head + 8 * h;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) q[s] = *(const u32x4_t *)(a + 16 * s);
-  }
+  // Whole rows pass between memory and the wave's registers through its quarter
+  // of LDS (before the first and after the last tile): a row's D / 8 pieces by
+  // as many lanes side by side, where the lane's own 16 bytes of 32 rows each
+  // would be a line a lane and load (64 prompts of 128 tokens, 32/8 heads of
+  // 128: 50 us that way, 44 this; no difference at thousands of tokens).  The
+  // pieces of a row are permuted so that neither side meets a bank twice.
+  constexpr int RPI = 64 / NC;  // rows of one access
+  auto piece_in_lds = [&](int r, int piece) __attribute__((always_inline)) {
+    return (u32x4_t *)(lds + wave * (32 * D * 2) + (r * NC + (piece ^ (r & 7))) * 16);
+  };
+  // Where the tile's row 32 * wave + r is in `x`, as elements (past the last
+  // row: the last).
+  auto row_offset = [&](const Rows &x, int r) __attribute__((always_inline)) {
+    const int at = min(r0 + 32 * wave + r, r_last), t = quotient(at, p.by_group);
+    return (int64_t)(w.q0 + t) * x.token + (int64_t)(head * p.group + at - t * p.group) * x.head;
+  };
+  // The piece of access i that lane `ln` moves, given its own row's offset.
+  auto piece_at = [&](const Rows &x, int64_t own, int i, int ln) __attribute__((always_inline)) {
+    const int r = i * RPI + ln / NC;
+    const uint32_t low = (uint32_t)__shfl((int)own, r, 64), high = (uint32_t)__shfl((int)(own >> 32), r, 64);
+    return x.data + (int64_t)((uint64_t)high << 32 | low) + 8 * (ln % NC);
+  };
+  auto lds_order = [&]() __attribute__((always_inline)) {  // LDS serves a wave's accesses in order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
 
   // ---- staging: of every tile a thread has piece c (8 dims) of the keys
   // ka .. ka+3 and half of piece c of the values of va .. va+7
@@ -208,6 +226,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   auto key_page = [&](int t, int a) __attribute__((always_inline)) { return PAGED ? page_of(start + t * BN + a) : 0; };
   int vpg = key_page(0, va);  // of the values in vraw
   int kpg_next = key_page(0, ka), vpg_next = key_page(1, va);
+  u32x4_t q[D / 16];
+  {
+    const int64_t own = row_offset(p.q, col);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) q[i] = *(const u32x4_t *)piece_at(p.q, own, i, lane);
+  }
   if (n_tiles > 0) {
     const auto load = fetch(0, kpg_next, 0, vpg);
     kpg_next = key_page(1, ka);
@@ -215,6 +239,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     for (int i = 0; i < 12; ++i) load(i);
   }
   if (tid == 0) s_odd = 0;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) *piece_in_lds(i * RPI + lane / NC, lane % NC) = q[i];
+  lds_order();
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) q[i] = *piece_in_lds(col, 2 * i + h);
   bool holes = false;
   if constexpr (PAGED) {
     int any = 0;
@@ -470,7 +499,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // ---- results: element 4q + i of product d is dim value_dim(d, q, i); for
   // each run of 8 dims (piece) a lane has all 8
   // piece_of: the piece of the lane's run x; (prod, elem): where its j-th dim is.
-  auto piece_of = [&](int x) __attribute__((always_inline)) { return D == 64 ? 4 * h + x : 8 * (x >> 2) + 4 * h + (x & 3); };
+  auto piece_of = [](int x, int h) __attribute__((always_inline)) { return D == 64 ? 4 * h + x : 8 * (x >> 2) + 4 * h + (x & 3); };
   auto prod = [](int j) __attribute__((always_inline)) { return D == 64 ? j >> 2 : D == 128 ? j >> 1 : j; };
   auto elem = [](int x, int j) __attribute__((always_inline)) {
     return D == 64 ? 4 * (j & 3) + x : D == 128 ? 4 * (2 * (j & 1) + (x >> 2)) + (x & 3) : x;
@@ -488,7 +517,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
         const int64_t slot = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          const int piece = piece_of(x);
+          const int piece = piece_of(x, h);
           uint32_t word[PW];
           float scale = 1.f;
           if constexpr (PAGED) {
@@ -566,13 +595,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     put(w.split);
     if (!add_parts(p, w, head, add, put)) return;
   }
-  if (!live) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key is zero
+  int ln = lane;
+  asm volatile("" : "+v"(ln));  // addresses made here, not held through the loop
+  const int64_t own = row_offset(p.out, ln & 31);
+  __syncthreads();  // the last tile has been read
 #pragma unroll
   for (int x = 0; x < D / 16; ++x) {
-    float v[8];
+    u32x4_t v;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = o[prod(j)][elem(x, j)];
-    store_row<BF16, 8>(p, w, row, head, 8 * piece_of(x), v, l);
+    for (int j = 0; j < 4; ++j)
+      v[j] = Half<BF16>::pack(o[prod(2 * j)][elem(x, 2 * j)] * inv, o[prod(2 * j + 1)][elem(x, 2 * j + 1)] * inv);
+    *piece_in_lds(ln & 31, piece_of(x, ln >> 5)) = v;
+  }
+  lds_order();
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const int r = i * RPI + ln / NC;
+    const u32x4_t v = *piece_in_lds(r, ln % NC);
+    uint16_t *y = piece_at(p.out, own, i, ln);
+    if (r0 + 32 * wave + r < rows) *(u32x4_t *)y = v;
   }
 }
 
