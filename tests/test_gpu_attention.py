@@ -319,6 +319,40 @@ def test_prompt_and_cache_agree():
     ref.check(x.run(), want, bound, "direct")
 
 
+@pytest.mark.parametrize("n", [3, 150])
+def test_rows_past_32_bit_offsets(n):
+    """Queries and results whose last rows are more than 2^32 bytes after their first: the same bits as dense ones."""
+    hq, hkv, d = 8, 2, 64
+    stride = -(-(2 ** 31 + 2 ** 20) // (n - 1)) // 8 * 8 + 8
+    x = Packed([n], hq, hkv, d, BF16, seed=15)
+    want = x.run()
+    far = [torch.empty((n - 1) * stride + hq * d, dtype=BF16, device="cuda").as_strided((n, hq, d), (stride, d, 1))
+           for _ in range(2)]
+    assert (n - 1) * stride * 2 > 2 ** 32
+    far[0].copy_(x.q)
+    got = ex.prompt_attention(far[0], x.k.cuda(), x.v.cuda(), x.cu.cuda(), out=far[1])
+    assert got is far[1] and same_bits(got, want)
+    cache = ex.KvCache.empty(3, 64, hkv, d, 16, BF16)
+    ex.cache_write(cache, x.k.cuda(), x.v.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"))
+    lens, table = torch.tensor([n], dtype=torch.int32).cuda(), torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    want = ex.paged_attention(cache, x.q.cuda(), x.cu.cuda(), lens, table)
+    assert same_bits(ex.paged_attention(cache, far[0], x.cu.cuda(), lens, table, out=far[1]), want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [3, 100])
+def test_a_nonfinite_query_row_stays_alone(n, d):
+    x = Packed([n, 40], 6, 2, d, BF16, seed=16)
+    want = x.run()
+    x.q[1, 4] = math.nan
+    x.q[2, 0, 7] = math.inf
+    got = x.run()
+    assert got[1, 4].isnan().all() and not got[2, 0].isfinite().all()
+    keep = torch.ones(n + 40, 6, dtype=torch.bool)
+    keep[1, 4] = keep[2, 0] = False
+    assert same_bits(got.cpu()[keep], want.cpu()[keep])
+
+
 def test_no_tokens():
     empty = torch.empty(0, 4, 64, dtype=BF16, device="cuda")
     cu = torch.zeros(3, dtype=torch.int32, device="cuda")
