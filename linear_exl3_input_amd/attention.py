@@ -144,12 +144,20 @@ def _ints(t: torch.Tensor, name: str, n: int, device) -> int:
     return t.data_ptr()
 
 
-def _out(out: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tensor:
+def _out(out: Optional[torch.Tensor], like: torch.Tensor, name: str) -> Tuple[torch.Tensor, _Rows]:
+    """`out`, or a new dense tensor like the (checked) `like`, and its view."""
     if out is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+        tokens, heads, dim = like.shape  # (strides as _rows gives them)
+        return out, _Rows(out.data_ptr(), heads * dim if tokens > 1 else 0, dim if heads > 1 else 0, heads)
     if out.shape != like.shape:
         raise ValueError(f"{name} has shape {tuple(out.shape)}, expected {tuple(like.shape)}")
-    return out
+    return out, _rows(out, name, like)
+
+
+def _same_device(r: "Rope", q: torch.Tensor) -> None:
+    if r.device != q.device:
+        raise ValueError(f"the rotations are on {r.device}, q on {q.device}")
 
 
 def split_heads(qkv: torch.Tensor, q_heads: int, kv_heads: int, head_dim: int):
@@ -171,7 +179,7 @@ class Rope:
             raise ValueError("table must be a contiguous float32 tensor [positions, rotary_dim/2, 2]")
         if not table.is_cuda:
             raise ValueError("table must be a GPU tensor")
-        self.table, self.interleaved = table, bool(interleaved)
+        self.table, self.interleaved, self.device = table, bool(interleaved), table.device
         self.positions, self.rotary_dim = table.shape[0], 2 * table.shape[1]
         self._view = _Rotary(table.data_ptr(), self.positions, self.rotary_dim, int(self.interleaved))
         self._ref = ctypes.byref(self._view)
@@ -285,13 +293,13 @@ def rope(r: Rope, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Te
     An output may be its input (in place)."""
     T, _, D = q.shape
     qr = _rows(q, "q")
-    q_out = _out(q_out, q, "q_out")
-    qo = _rows(q_out, "q_out", q)
+    _same_device(r, q)
+    q_out, qo = _out(q_out, q, "q_out")
     kr = ko = None
     if k is not None:
         kr = ctypes.byref(_rows(k, "k", q))
-        k_out = _out(k_out, k, "k_out")
-        ko = ctypes.byref(_rows(k_out, "k_out", k))
+        k_out, ko = _out(k_out, k, "k_out")
+        ko = ctypes.byref(ko)
     elif k_out is not None:
         raise ValueError("k_out without k")
     _check(_lib().exl3_rope(r._ref, _ints(positions, "positions", T, q.device), T, D, _dtype_id(q.dtype, "q"),
@@ -325,9 +333,9 @@ def rope_cache_write(cache: KvCache, r: Rope, positions: torch.Tensor, slots: to
     qr, kr, vr = _cache_rows(cache, q, "q"), _cache_rows(cache, k, "k"), _cache_rows(cache, v, "v")
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError(f"q has {T} tokens, k {k.shape[0]}, v {v.shape[0]}")
-    q_out = _out(q_out, q, "q_out")
-    qo = _rows(q_out, "q_out", q)
-    ko = ctypes.byref(_rows(_out(k_out, k, "k_out"), "k_out", k)) if k_out is not None else None
+    _same_device(r, q)
+    q_out, qo = _out(q_out, q, "q_out")
+    ko = ctypes.byref(_out(k_out, k, "k_out")[1]) if k_out is not None else None
     _check(_lib().exl3_rope_cache_write(cache._ref, r._ref, _ints(positions, "positions", T, q.device),
                                         _ints(slots, "slots", T, q.device), T, ctypes.byref(qr), ctypes.byref(qo),
                                         ctypes.byref(kr), ko, ctypes.byref(vr), _raw_stream(cache.device.index)))
@@ -377,8 +385,7 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
             page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
         raise ValueError(f"page_table must be int32 [{B}, width] with dense rows on {dev}, got {page_table.dtype} "
                          f"{tuple(page_table.shape)}")
-    out = _out(out, q, "out")
-    o = _rows(out, "out", q)
+    out, o = _out(out, q, "out")
     L = _lib()
     need = L.exl3_attention_workspace_bytes(B, T, H, cache.heads, D)
     stream = _raw_stream(dev.index)
@@ -397,8 +404,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     T, H, D = q.shape
     B = cu_seqlens.shape[0] - 1
     qr, kr, vr = _rows(q, "q"), _rows(k, "k", q), _rows(v, "v", q)
-    out = _out(out, q, "out")
-    o = _rows(out, "out", q)
+    out, o = _out(out, q, "out")
     L = _lib()
     need = L.exl3_attention_workspace_bytes(B, T, H, k.shape[1], D)
     stream = _raw_stream(q.device.index)

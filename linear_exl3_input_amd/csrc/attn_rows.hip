@@ -20,7 +20,7 @@ namespace exl3 {
 // more than the 4.97 TB/s of a copy, as the output stays in the last cache);
 // 16300 tokens written to 8 bits and read back, 8 heads of 128, 46 us for both
 // (202 MB, 4.4 TB/s); one step of 16 tokens, 24/4 heads of 256, 3.2 us on the
-// GPU and 9.7 with the host's call.
+// GPU and 9.2 with the host's call.
 template <bool BF16, int D, int BITS>
 __device__ __forceinline__ void write_codes(const uint32_t (&w)[4], uint8_t *codes, uint8_t *scales, int c) {
   if constexpr (BITS == 16) {

@@ -218,3 +218,15 @@ def test_slots_of_positions():
     table = torch.tensor([[4, 2, -1], [7, 9, 0]], dtype=torch.int32, device="cuda")
     got = cache.slots(table, torch.tensor([0, 0, 0, 1, 1], device="cuda"), torch.tensor([0, 17, 40, 31, 32], device="cuda"))
     assert got.tolist() == [64, 33, -1, 159, 0] and got.dtype == torch.int32
+
+
+def test_rotations_on_another_device_are_refused():
+    r = ex.Rope.make(64, 1e4, 32)
+    x = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    cache = ex.KvCache.empty(1, 16, 4, 64)
+    at = torch.zeros(2, dtype=torch.int32, device="cuda")
+    r.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="the rotations are on cuda:1, q on cuda:0"):
+        ex.rope(r, at, x)
+    with pytest.raises(ValueError, match="the rotations are on cuda:1, q on cuda:0"):
+        ex.rope_cache_write(cache, r, at, at, x, x, x)
