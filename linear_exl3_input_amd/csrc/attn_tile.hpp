@@ -171,7 +171,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   uint32_t kraw[4][PW], vraw[8][HW];
   uint32_t ksc[4], vsc[8];
   // Packed rows: a descriptor that ends with tile t's last key, so rows past it
-  // read as zeros (and nothing is read past the last tile).
+  // read as zeros (and nothing is read past the last tile).  The check sees the
+  // vector offset alone, so a row's place is there and not in the scalar one.
   auto packed = [&](const Rows &x, int t) __attribute__((always_inline)) {
     const int n = min(hi - start - t * BN, BN);  // the host keeps a tile's rows within 2^31 bytes
     return __builtin_amdgcn_make_buffer_rsrc(x.data + head * x.head + (int64_t)(w.q0 + start + t * BN) * x.token, (short)0,
@@ -205,16 +206,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     } else {
       const auto krs = packed(p.k, tk), vrs = packed(p.v, tv);
       const int kstep = (int)p.k.token * 2, vstep = (int)p.v.token * 2;
-      return [&, krs, vrs, kstep, vstep](int i) __attribute__((always_inline)) {
+      int kat = ka * kstep + c * 16, vat = va * vstep + c * 16 + half * 8;
+      asm volatile("" : "+v"(kat), "+v"(vat));  // the rows' offsets made at the loads, not held through the loop
+      return [&, krs, vrs, kstep, vstep, kat, vat](int i) __attribute__((always_inline)) {
         if (i < 4) {
           const u32x4_t x = __builtin_bit_cast(
-              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(krs, ka * kstep + c * 16, i * kstep, 0));
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(krs, kat + i * kstep, 0, 0));
 #pragma unroll
           for (int y = 0; y < 4; ++y) kraw[i][y] = x[y];
         } else {
           i -= 4;
           const u32x2_t x = __builtin_bit_cast(
-              u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(vrs, va * vstep + c * 16 + half * 8, i * vstep, 0));
+              u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(vrs, vat + i * vstep, 0, 0));
           vraw[i][0] = x.x, vraw[i][HW - 1] = x.y;
         }
       };
