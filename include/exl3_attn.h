@@ -113,9 +113,9 @@ exl3_status exl3_cache_read(const exl3_kv_cache *c, const int32_t *slots, int32_
  * j % page_size of page page_table[s][j / page_size] (int32, row stride
  * page_table_stride, width page_table_width); a page outside 0..pages-1, or
  * past the width, is a hole whose keys nobody sees.  Query head h reads the
- * cache's head h / (q.heads / heads).  Rows that see no key are zero.  A cu_q
- * that is not as above leaves out's values undefined and may leave counters in
- * the workspace that have to be cleared before its next use.
+ * cache's head h / (q.heads / heads).  Rows that see no key are zero.  An
+ * offset in cu_q counts as at least those before it and at most tokens; rows
+ * that then belong to no sequence are not written.
  *   out = softmax(scale * q k^T) v, products in the cache's dtype with fp32
  * sums, the probabilities rounded to that type for the second product. */
 exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out, const int32_t *cu_q,

@@ -99,6 +99,16 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
   return v;
 }
+// Inclusive maxima of values that are not negative, likewise.
+__device__ __forceinline__ int wave_inclusive_max(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));
+  return v;
+}
 __device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_inclusive_sum(v), 63); }
 __device__ __forceinline__ float wave_sum(float v) {
   auto add = [&](int moved) __attribute__((always_inline)) { v += __builtin_bit_cast(float, moved); };
@@ -138,22 +148,36 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
   struct Seq {
     int q0, ql, kv, tiles, span;
   };
-  auto load = [&](int s) __attribute__((always_inline)) -> Seq {
-    Seq x = {0, 0, 0, 0, 0};
+  // Sequences s0 + lane; `from` is where s0 starts at the earliest, then where
+  // the 64 after them do.  An offset below an earlier one counts as that one:
+  // sequences never overlap, so what was said above holds whatever cu has.
+  auto load = [&](int s0, int &from) __attribute__((always_inline)) -> Seq {
+    const int s = s0 + lane;
+    int a = 0, b = 0, kv = 0;
     if (s < p.batch) {
-      const int a = min(max(p.cu[s], 0), p.tokens), b = min(max(p.cu[s + 1], 0), p.tokens);
-      x.q0 = a;
-      x.ql = max(0, b - a);
-      x.kv = p.kv_len ? max(0, p.kv_len[s]) : x.ql;
-      x.tiles = (int)(((int64_t)x.ql * p.group + R - 1) / R);
-      // a tile's rows are at most R tokens; its keys start at a multiple of 32
-      x.span = p.kv_len ? min(x.kv, p.table_keys) : x.kv;
-      if (p.window > 0) x.span = min(x.span, p.window + R + 32);
+      a = p.cu[s], b = p.cu[s + 1];
+      if (p.kv_len) kv = p.kv_len[s];
     }
+    a = max(from, wave_inclusive_max(min(max(a, 0), p.tokens)));
+    b = max(a, min(b, p.tokens));
+    from = __builtin_amdgcn_readlane(b, 63);
+    Seq x;
+    x.q0 = a;
+    x.ql = b - a;
+    x.kv = p.kv_len ? max(0, kv) : x.ql;
+    x.tiles = (int)(((int64_t)x.ql * p.group + R - 1) / R);
+    // a tile's rows are at most R tokens; its keys start at a multiple of 32
+    x.span = p.kv_len ? min(x.kv, p.table_keys) : x.kv;
+    if (p.window > 0) x.span = min(x.span, p.window + R + 32);
     return x;
   };
-  const Seq head = load(lane);  // the first 64 sequences, mostly all of them
-  auto seq_at = [&](int s0) __attribute__((always_inline)) { return s0 == 0 ? head : load(s0 + lane); };
+  int head_end = 0, from;
+  const Seq head = load(0, head_end);  // the first 64 sequences, mostly all of them
+  auto seq_at = [&](int s0) __attribute__((always_inline)) {
+    if (s0 > 0) return load(s0, from);
+    from = head_end;
+    return head;
+  };
   int C = 0x7FFFFFFF;
   auto splits_of = [&](const Seq &x) __attribute__((always_inline)) -> int {
     return x.span > C ? (int)(((uint32_t)x.span + (uint32_t)C - 1u) / (uint32_t)C) : 1;
@@ -198,10 +222,8 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       w.q_len = __builtin_amdgcn_readlane(x.ql, l);
       w.kv_len = __builtin_amdgcn_readlane(x.kv, l);
       w.part = w.splits > 1 ? pbase + __builtin_amdgcn_readlane(pincl - parts, l) + at : 0;
-      // (sequences that overlap, which cu must not have, can make more tiles and
-      // parts than there are numbers or room for; those are left out)
-      if (at < 0 || w.tile >= __builtin_amdgcn_readlane(x.tiles, l)) return false;
-      return w.splits == 1 || (w.part >= w.split && w.part - w.split + w.splits <= p.part_cap);
+      // (lengths that are written while the call runs could make more parts than there is room for)
+      return w.splits == 1 || w.part - w.split + w.splits <= p.part_cap;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
     pbase += __builtin_amdgcn_readlane(pincl, 63);
