@@ -281,10 +281,17 @@ class KvCache:
         return cls(k, v, ks, vs, dtype)
 
     def slots(self, page_table: torch.Tensor, seq: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
-        """The int32 slots of tokens at `positions` of the sequences `seq` (rows of the page table)."""
-        p = positions.long()
-        page = page_table[seq.long(), p // self.page_size].long()
-        return torch.where(page < 0, torch.full_like(page, -1), page * self.page_size + p % self.page_size).int()
+        """The int32 slots of tokens at `positions` of the sequences `seq` (rows of the page table); -1 where there is
+        none: a hole of the table, or a position or sequence outside it (padding rows)."""
+        rows, width = page_table.shape
+        if rows == 0 or width == 0:
+            return torch.full_like(positions, -1, dtype=torch.int32)
+        at = positions // self.page_size
+        s, i = seq.clamp(0, rows - 1), at.clamp(0, width - 1)
+        page = page_table[s, i]
+        missing = (s != seq) | (i != at) | (page.clamp(0, self.pages - 1) != page)
+        slot = torch.add(positions % self.page_size, page, alpha=self.page_size)
+        return torch.where(missing, -1, slot).int()
 
 
 def rope(r: Rope, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Tensor] = None,

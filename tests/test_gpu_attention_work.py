@@ -88,3 +88,26 @@ def test_more_sequences_than_a_wave_has_lanes(batch):
     a, b = rows.start, rows.stop
     o, e = ref.attend(*(x[a:b].cpu().double() for x in (q, k, v)), ref.mask(b - a, b - a), 0.125, BF16)
     ref.check(wide[a:b], o, e, "the sequences around the fall")
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_padding_rows_leave_the_cache_alone(bits):
+    """A step of fixed size whose last rows are padding, at position -1 or of no sequence, or past the table."""
+    cache = ex.KvCache.empty(6, 16, 2, 128, bits)
+    every = torch.arange(96, dtype=torch.int32, device="cuda")
+    x = normal(10, (96, 2, 128)).cuda()
+    ex.cache_write(cache, x, x, every)
+    before = ex.cache_read(cache, every)
+    table = ints([[5, 1, 3], [0, 2, 4]])
+    seq, pos = ints([0, 1, 1, -1, 2, 0]), ints([17, 40, -1, 3, 3, 48])
+    slots = cache.slots(table, seq, pos)
+    assert slots.tolist() == [17, 72, -1, -1, -1, -1]
+    r = ex.Rope.make(128, 1e4, 100)
+    y = normal(11, (6, 2, 128)).cuda()
+    ex.rope_cache_write(cache, r, pos, slots, y, y, y)
+    after = ex.cache_read(cache, every)
+    keep = [i for i in range(96) if i not in (17, 72)]
+    for a, b in zip(after, before):
+        assert same_bits(a[keep], b[keep])
+    for i, s in ((0, 17), (1, 72)):
+        assert torch.equal(after[1][s].double().cpu(), ref.quantise(y[i].cpu(), bits))
