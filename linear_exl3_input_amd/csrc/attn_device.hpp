@@ -62,7 +62,8 @@ __device__ __forceinline__ int quotient(int n, const Divisor &d) {
 // ------------------------------------------------------- codes and scales
 
 // The scale of byte s as a float: 2^(s - 127).  255, a block that held a NaN
-// or an infinity, becomes a NaN, and the conversions give NaN for it.
+// or an infinity, becomes a NaN, and the conversions give NaN for it.  (They
+// take the exponent alone, so the zero made of 0 counts as 2^-127.)
 __device__ __forceinline__ float scale_of(uint32_t s) {
   return __uint_as_float(s == 255u ? 0x7FC00000u : s << 23);
 }

@@ -274,37 +274,33 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // Values of a tile that some row does not see whole: what lies outside the
   // range or in a hole counts as zero, and so do infinities and NaN that some
   // rows must not see (0 * inf would reach them through the product); the rows
-  // that do see them get them at the end.
+  // that do see them get them at the end.  (Those of codes: finite_v.)
   auto clean_v = [&](int t, int pg) __attribute__((always_inline)) {
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const bool in = (uint32_t)(start + t * BN + va + i - lo) < (uint32_t)(hi - lo) && (!PAGED || pg >= 0);
-      if constexpr (CB < 16) {
-        const bool bad = vsc[i] == 255u;  // the only codes that are not finite
-        odd = odd || (in && bad);
-        if (!in || bad) {
-          vsc[i] = 127u;
 #pragma unroll
-          for (int y = 0; y < HW; ++y) vraw[i][y] = 0u;
-        }
-      } else {
-#pragma unroll
-        for (int y = 0; y < HW; ++y) {
-          vraw[i][y] = in ? vraw[i][y] : 0u;
+      for (int y = 0; y < HW; ++y) {
+        vraw[i][y] = in ? vraw[i][y] : 0u;
+        if constexpr (CB == 16) {
           odd = odd || odd_pair<BF16>(vraw[i][y]);
           vraw[i][y] = finite_pair<BF16>(vraw[i][y]);
         }
       }
+      if constexpr (CB < 16) vsc[i] = in ? vsc[i] : 127u;
     }
     if (odd) s_odd = 1;
+  };
+  auto values_of = [&](int t) __attribute__((always_inline)) {  // where the thread's values of tile t are
+    return lds + (t & 1) * G::BUF + G::K_BYTES + ((va >> 3) * D + 4 * half * NC + c) * 16;
   };
   // Dims 2j and 2j + 1 (j 0..1) of the thread's values, keys side by side.
   auto put_v = [&](int t, int j) __attribute__((always_inline)) {
     uint32_t x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = pair_at<BF16, CB>(vraw[i], j, CB < 16 ? scale_of(vsc[i]) : 1.f);
-    uint8_t *buf = lds + (t & 1) * G::BUF + G::K_BYTES + ((va >> 3) * D + 4 * half * NC + c) * 16;
+    uint8_t *buf = values_of(t);
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       u32x4_t v;
@@ -312,6 +308,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
       for (int z = 0; z < 4; ++z) v[z] = __builtin_amdgcn_perm(x[2 * z + 1], x[2 * z], y ? 0x07060302u : 0x05040100u);
       *(u32x4_t *)(buf + (2 * j + y) * NC * 16) = v;
     }
+  };
+  // Codes may stand for infinities and NaN in several ways (a NaN code, a block
+  // that held one, a scale that overflows the type), so they are looked for among
+  // the decoded values, in LDS, where the thread has put them: on the raw codes
+  // this costs registers that the loop does not have (chunks over 8 bits 685 ->
+  // 715 us, this way 690; 16-bit values in LDS instead of above: windows with
+  // heads of 256 277 -> 294).
+  auto finite_v = [&](int t) __attribute__((always_inline)) {
+    bool odd = false;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      u32x4_t *at = (u32x4_t *)(values_of(t) + j * NC * 16);
+      u32x4_t v = *at;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        odd = odd || odd_pair<BF16>(v[y]);
+        v[y] = finite_pair<BF16>(v[y]);
+      }
+      *at = v;
+    }
+    if (odd) s_odd = 1;
   };
 
   float16_t o[DT];
@@ -471,6 +488,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     float keep;
     if (!whole_tile(0)) clean_v(0, vpg);
     score_and_stage(0);
+    if (CB < 16 && !whole_tile(0)) finite_v(0);
     {
       const auto load = fetch(2, kpg_next, 1, vpg_next);
 #pragma unroll
@@ -484,6 +502,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     for (int t = 1; t < n_tiles; ++t) {
       if (!whole_tile(t)) clean_v(t, vpg);
       score_and_stage(t);
+      if (CB < 16 && !whole_tile(t)) finite_v(t);
       int grew = __builtin_amdgcn_readfirstlane((int)settle(t, keep));
       asm volatile("" : "+s"(grew));  // one block of products and vector work for both cases
       product_and_weigh(t - 1, fetch(t + 2, kpg_next, t + 1, vpg_next));
