@@ -343,10 +343,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, s[n][t][i]);
       top = column_max(top);
-      // The running maximum moves, and o is scaled, only when some row's grew by
-      // more than 2^8: probabilities reach at most 2^8, within range for both
-      // types, and the sums are fp32.
-      if (__any(top > m[n] + 8.f)) {
+      if (__any(top > m[n] + PROB_LAG)) {
         const float grown = __builtin_fmaxf(m[n], top);
         const float keep = grown == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[n] - grown);
         m[n] = grown;
@@ -354,7 +351,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 #pragma unroll
         for (int j = 0; j < DV; ++j) o[n][j] *= keep;
       }
-      const float base = m[n] == -INFINITY ? 0.f : m[n];
+      const float base = prob_base<BF16>(m[n]);
       float pf[8];
       float sum = 0.f;
 #pragma unroll
@@ -365,8 +362,6 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
           sum += pf[4 * t + i];
         }
       l[n] += sum;
-      // rounded to the type for the product (error 2^-9 or 2^-12 of each
-      // term, no larger than the output's own rounding); l sums them unrounded
       pr[n] = (u32x4_t){Half<BF16>::pack(pf[0], pf[1]), Half<BF16>::pack(pf[2], pf[3]), Half<BF16>::pack(pf[4], pf[5]),
                         Half<BF16>::pack(pf[6], pf[7])};
     }

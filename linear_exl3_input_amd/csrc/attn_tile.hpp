@@ -369,9 +369,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // The mask, and the running maximum: it moves only when some row's grew by
-  // more than 2^8, so probabilities reach at most 2^8 (within range for both
-  // types, and the sums are fp32).  True when it did: o then has to be
+  // The mask, and the running maximum.  True when it moved: o then has to be
   // multiplied by `keep`.
   auto settle = [&](int t, float &keep) __attribute__((always_inline)) -> bool {
     const int k0 = start + t * BN;
@@ -394,7 +392,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[n][i]);
     top = pair_max(top) * p.scale_log2;
-    if (!__any(top > m + 8.f)) return false;
+    if (!__any(top > m + PROB_LAG)) return false;
     const float grown = __builtin_fmaxf(m, top);
     keep = grown == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - grown);
     m = grown;
@@ -414,10 +412,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
           o[d] = mfma32<BF16>(a, pr[n][t8], o[d]);
         }
   };
-  // Probabilities are rounded to the type for the product (an error no larger
-  // than the output's own rounding); the sum takes them unrounded.
+  // Probabilities, rounded to the type for the product; the sum takes them unrounded.
   auto weigh = [&]() __attribute__((always_inline)) {
-    const float base = m == -INFINITY ? 0.f : m;
+    const float base = prob_base<BF16>(m);
 #pragma unroll
     for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -443,7 +440,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     u32x4_t ring[READS];
     u32x4_t was[NS][2];
     float f[16 * NS], sum[2] = {0.f, 0.f};
-    const float base = m == -INFINITY ? 0.f : m;
+    const float base = prob_base<BF16>(m);
 #pragma unroll
     for (int n = 0; n < NS; ++n) was[n][0] = pr[n][0], was[n][1] = pr[n][1];
 #pragma unroll
