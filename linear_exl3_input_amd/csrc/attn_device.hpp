@@ -73,6 +73,9 @@ __device__ __forceinline__ float prob_base(float m) {
   return m == -INFINITY ? 0.f : m - PROB_LIFT<BF16>;
 }
 
+// The workgroup's number in a grid of grid_of.
+__device__ __forceinline__ uint32_t workgroup() { return blockIdx.y << GRID_X_LOG2 | blockIdx.x; }
+
 __device__ __forceinline__ int quotient(int n, const Divisor &d) {
   return d.mul == 0u ? n : (int)(__umulhi((uint32_t)n, d.mul) >> d.shift);
 }

@@ -14,7 +14,7 @@ int64_t grid_items(const AttnParams &p, int R) {
 
 template <bool BF16, int BITS, int NT>
 hipError_t small_of(const AttnParams &p, hipStream_t s) {
-  const dim3 grid((unsigned)(grid_items(p, 16 * NT) * p.heads_kv));
+  const dim3 grid = grid_of(grid_items(p, 16 * NT) * p.heads_kv);
   hipLaunchKernelGGL((attn_small_kernel<BF16, EXL3_HEAD_DIM, BITS, NT>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
@@ -31,7 +31,7 @@ hipError_t small_bits(int bits, const AttnParams &p, hipStream_t s) {
 
 template <bool BF16, int BITS>
 hipError_t tile_of(const AttnParams &p, hipStream_t s) {
-  const dim3 grid((unsigned)(grid_items(p, ATTN_TILE_ROWS) * p.heads_kv));
+  const dim3 grid = grid_of(grid_items(p, ATTN_TILE_ROWS) * p.heads_kv);
   hipLaunchKernelGGL((attn_tile_kernel<BF16, EXL3_HEAD_DIM, BITS>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }

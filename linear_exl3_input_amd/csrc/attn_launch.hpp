@@ -22,6 +22,15 @@ struct Divisor {
   }
 };
 
+// A launch has fewer than 2^32 threads along x, so workgroups (of 256) past 2^23
+// go on along y.  The last row of that grid can have some too many.
+constexpr int GRID_X_LOG2 = 23;
+inline dim3 grid_of(int64_t workgroups) {
+  const int64_t most = 1ll << GRID_X_LOG2;
+  return workgroups <= most ? dim3((unsigned)workgroups)
+                            : dim3((unsigned)most, (unsigned)((workgroups + most - 1) >> GRID_X_LOG2));
+}
+
 // Strided rows of 16-bit values; strides in elements.
 struct Rows {
   uint16_t *data;

@@ -71,7 +71,7 @@ template <bool BF16, int D, int BITS>
 __global__ __launch_bounds__(256) void rows_kernel(RowsParams p) {
   constexpr int LPR = D / 8;  // lanes per row
   const int c = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const int64_t row = (int64_t)workgroup() * (256 / LPR) + threadIdx.x / LPR;
   const int H = p.hq + p.hk + p.hv;
   if (row >= (int64_t)p.tokens * H) return;  // whole rows leave: the quads below stay full
   const uint32_t t = (uint32_t)row / (uint32_t)H;
@@ -145,7 +145,7 @@ template <bool BF16, int D, int BITS>
 __global__ __launch_bounds__(256) void cache_read_kernel(ReadParams p) {
   constexpr int LPR = D / 8;
   const int c = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const int64_t row = (int64_t)workgroup() * (256 / LPR) + threadIdx.x / LPR;
   const int H = 2 * p.cache.heads;
   if (row >= (int64_t)p.n * H) return;
   const uint32_t t = (uint32_t)row / (uint32_t)H;
@@ -194,7 +194,7 @@ template <bool BF16, int D>
 hipError_t rows_of(int bits, const RowsParams &p, hipStream_t s) {
   constexpr int RPB = 256 / (D / 8);
   const int64_t rows = (int64_t)p.tokens * (p.hq + p.hk + p.hv);
-  const dim3 grid((unsigned)((rows + RPB - 1) / RPB)), block(256);
+  const dim3 grid = grid_of((rows + RPB - 1) / RPB), block(256);
   switch (bits) {
     case 0: hipLaunchKernelGGL((rows_kernel<BF16, D, 0>), grid, block, 0, s, p); break;
     case 4: hipLaunchKernelGGL((rows_kernel<BF16, D, 4>), grid, block, 0, s, p); break;
@@ -208,7 +208,7 @@ template <bool BF16, int D>
 hipError_t read_of(int bits, const ReadParams &p, hipStream_t s) {
   constexpr int RPB = 256 / (D / 8);
   const int64_t rows = (int64_t)p.n * 2 * p.cache.heads;
-  const dim3 grid((unsigned)((rows + RPB - 1) / RPB)), block(256);
+  const dim3 grid = grid_of((rows + RPB - 1) / RPB), block(256);
   switch (bits) {
     case 4: hipLaunchKernelGGL((cache_read_kernel<BF16, D, 4>), grid, block, 0, s, p); break;
     case 8: hipLaunchKernelGGL((cache_read_kernel<BF16, D, 8>), grid, block, 0, s, p); break;

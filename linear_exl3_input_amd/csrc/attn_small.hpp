@@ -161,8 +161,8 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const int head = blockIdx.x % p.heads_kv;
-  const int item = blockIdx.x / p.heads_kv;
+  const int head = workgroup() % p.heads_kv;
+  const int item = workgroup() / p.heads_kv;
   Work w;
   if (!find_work<R>(p, item, lane, w)) return;
 

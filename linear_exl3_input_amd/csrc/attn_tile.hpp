@@ -97,8 +97,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: a wave stages keys or values
   const int col = lane & 31, h = lane >> 5;
-  const int head = blockIdx.x % p.heads_kv;
-  const int item = blockIdx.x / p.heads_kv;
+  const int head = workgroup() % p.heads_kv;
+  const int item = workgroup() / p.heads_kv;
   Work w;
   if (!find_work<R>(p, item, lane, w)) return;
   const int rows = w.q_len * p.group;
