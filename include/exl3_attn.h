@@ -9,6 +9,8 @@
  *   - Pointers are DEVICE pointers unless marked HOST.  The caller owns every
  *     buffer and the stream; no call allocates, frees or synchronizes, so all
  *     calls may be captured in a HIP graph.
+ *   - Launches are made on the calling thread's current device, which has to
+ *     be the buffers' and the stream's.
  *   - Every argument that is known on the host is checked before any HIP
  *     call; on error nothing is enqueued and exl3_last_error() names the
  *     failed check.  Values in device memory (positions, slots, lengths, page

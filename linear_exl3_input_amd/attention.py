@@ -105,6 +105,9 @@ def _dtype_id(dtype: torch.dtype, name: str) -> int:
 # with a shape, dtype and device 2.0 us), the workspace's lock only when there
 # is something to do.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+# The library launches on the current device and plans for it: a call whose
+# tensors are on another one makes that current first.
+_current_device = torch._C._cuda_getDevice
 
 
 def _scratch(nbytes: int, device: torch.device, stream: int) -> Tuple[Optional[int], int]:
@@ -301,6 +304,9 @@ def rope(r: Rope, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Te
     T, _, D = q.shape
     qr = _rows(q, "q")
     _same_device(r, q)
+    if _current_device() != q.device.index:
+        with torch.cuda.device(q.device):
+            return rope(r, positions, q, k, q_out, k_out)
     q_out, qo = _out(q_out, q, "q_out")
     kr = ko = None
     if k is not None:
@@ -323,6 +329,9 @@ def _cache_rows(cache: KvCache, t: torch.Tensor, name: str) -> _Rows:
 
 def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Writes k and v [tokens, heads, head_dim] to the cache's slots (int32 [tokens]; -1: skipped)."""
+    if _current_device() != cache.device.index:
+        with torch.cuda.device(cache.device):
+            return cache_write(cache, k, v, slots)
     kr, vr = _cache_rows(cache, k, "k"), _cache_rows(cache, v, "v")
     T = k.shape[0]
     if v.shape[0] != T:
@@ -336,6 +345,9 @@ def rope_cache_write(cache: KvCache, r: Rope, positions: torch.Tensor, slots: to
                      k_out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """rope(q, k) and cache_write(rotated k, v) in one launch, with the same bits; returns the rotated q.  The rotated
     k also goes to k_out when that is given."""
+    if _current_device() != cache.device.index:
+        with torch.cuda.device(cache.device):
+            return rope_cache_write(cache, r, positions, slots, q, k, v, q_out, k_out)
     T = q.shape[0]
     qr, kr, vr = _cache_rows(cache, q, "q"), _cache_rows(cache, k, "k"), _cache_rows(cache, v, "v")
     if k.shape[0] != T or v.shape[0] != T:
@@ -352,6 +364,9 @@ def rope_cache_write(cache: KvCache, r: Rope, positions: torch.Tensor, slots: to
 def cache_read(cache: KvCache, slots: torch.Tensor, k_out: Optional[torch.Tensor] = None,
                v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The keys and values of the slots (int32 [n]) as [n, heads, head_dim] of the cache's dtype; -1 reads as zeros."""
+    if _current_device() != cache.device.index:
+        with torch.cuda.device(cache.device):
+            return cache_read(cache, slots, k_out, v_out)
     n = slots.shape[0]
     shape = (n, cache.heads, cache.head_dim)
     if k_out is None:
@@ -384,6 +399,9 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
     (int32 [batch]); its last row is at position kv_len[s]-1.  A row sees the keys up to its own position (window > 0:
     the last `window` of them).  page_table int32 [batch, width]: the page of keys j*page_size...; pages that are not
     the cache's (-1) are holes.  scale defaults to head_dim^-0.5.  Rows that see no key are zero."""
+    if _current_device() != cache.device.index:
+        with torch.cuda.device(cache.device):
+            return paged_attention(cache, q, cu_q, kv_len, page_table, scale, window, out)
     T, H, D = q.shape
     B = kv_len.shape[0]
     dev = cache.device
@@ -411,6 +429,9 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     T, H, D = q.shape
     B = cu_seqlens.shape[0] - 1
     qr, kr, vr = _rows(q, "q"), _rows(k, "k", q), _rows(v, "v", q)
+    if _current_device() != q.device.index:
+        with torch.cuda.device(q.device):
+            return prompt_attention(q, k, v, cu_seqlens, causal, window, scale, out)
     out, o = _out(out, q, "out")
     L = _lib()
     need = L.exl3_attention_workspace_bytes(B, T, H, k.shape[1], D)
