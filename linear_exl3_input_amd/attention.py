@@ -158,6 +158,13 @@ def _out(out: Optional[torch.Tensor], like: torch.Tensor, name: str) -> Tuple[to
     return out, _rows(out, name, like)
 
 
+def _window(window: int) -> int:
+    """window for the library, which would take a number past 32 bits for what is left of it."""
+    if not 0 <= window <= 1 << 30:
+        raise ValueError(f"window={window}, must be 0 (none) to {1 << 30}")
+    return window
+
+
 def _same_device(r: "Rope", q: torch.Tensor) -> None:
     if r.device != q.device:
         raise ValueError(f"the rotations are on {r.device}, q on {q.device}")
@@ -417,7 +424,8 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
     ws, wsn = _scratch(need, dev, stream)
     _check(L.exl3_paged_attention(cache._ref, ctypes.byref(qr), ctypes.byref(o), _ints(cu_q, "cu_q", B + 1, dev),
                                   _ints(kv_len, "kv_len", B, dev), page_table.data_ptr(), page_table.stride(0),
-                                  page_table.shape[1], B, T, D ** -0.5 if scale is None else scale, window, ws, wsn, stream))
+                                  page_table.shape[1], B, T, D ** -0.5 if scale is None else scale, _window(window), ws, wsn,
+                                  stream))
     return out
 
 
@@ -439,5 +447,5 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     ws, wsn = _scratch(need, q.device, stream)
     _check(L.exl3_prompt_attention(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(o),
                                    _ints(cu_seqlens, "cu_seqlens", B + 1, q.device), B, T, D, _dtype_id(q.dtype, "q"),
-                                   int(causal), window, D ** -0.5 if scale is None else scale, ws, wsn, stream))
+                                   int(causal), _window(window), D ** -0.5 if scale is None else scale, ws, wsn, stream))
     return out

@@ -1,10 +1,11 @@
-"""The attention binding's own arithmetic on the CPU: slots of positions."""
+"""The attention binding's own arithmetic and checks on the CPU: slots of positions, windows."""
 from types import SimpleNamespace
 
 import pytest
 import torch
 
 import linear_exl3_input_amd as ex
+from linear_exl3_input_amd import attention as at
 
 
 def slots(pages, page_size, table, seq, positions):
@@ -48,3 +49,26 @@ def test_the_last_slot_of_the_largest_cache():
     pages = (2 ** 31 - 1) // 1024
     table = torch.tensor([[pages - 1]], dtype=torch.int32)
     assert slots(pages, 1024, table, torch.tensor([0]), torch.tensor([1023])).item() == pages * 1024 - 1
+
+
+@pytest.mark.parametrize("window", [-1, 2 ** 30 + 1, 2 ** 32, 2 ** 32 + 1, 2 ** 63 - 1])
+def test_windows_that_do_not_fit_are_refused(window):
+    """2^32 + 1 would be a window of 1 in 32 bits, 2^32 none at all."""
+    with pytest.raises(ValueError, match=f"window={window}, must be 0"):
+        at._window(window)
+
+
+def test_windows_that_fit_pass():
+    assert [at._window(w) for w in (0, 1, 4096, 2 ** 30)] == [0, 1, 4096, 2 ** 30]
+
+
+@pytest.mark.gpu
+def test_calls_refuse_windows_that_do_not_fit():
+    q = torch.randn(3, 4, 64, device="cuda").bfloat16()
+    cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    cache = ex.KvCache.empty(1, 16, 4, 64)
+    for window in (2 ** 32, 2 ** 32 + 1):
+        with pytest.raises(ValueError, match="window="):
+            ex.prompt_attention(q, q, q, cu, window=window)
+        with pytest.raises(ValueError, match="window="):
+            ex.paged_attention(cache, q, cu, cu[1:], cu[:1].view(1, 1), window=window)
