@@ -197,35 +197,60 @@ class Rope:
     @classmethod
     def make(cls, rotary_dim: int, base: float, positions: int, interleaved: bool = False, linear: float = 1.0,
              ntk: float = 1.0, yarn: Optional[Tuple[float, int]] = None, yarn_turns: Tuple[float, float] = (1.0, 32.0),
-             yarn_gain: Optional[float] = None, device="cuda") -> "Rope":
+             yarn_gain: Optional[float] = None, yarn_ramp: str = "pairs", device="cuda") -> "Rope":
         """Frequencies base^(-2i/rotary_dim), stretched for contexts longer than trained:
 
         linear f: every position is divided by f.
         ntk f: the base becomes base * f^(rotary_dim / (rotary_dim - 2)), so the slowest pair slows by f
             and the fastest stays.
         yarn (f, n): pairs that turn fewer than yarn_turns[0] times in the n trained positions slow by f,
-            those that turn more than yarn_turns[1] times stay, with a linear ramp between; cosines and
-            sines are multiplied by yarn_gain (default 0.1 ln f + 1).
+            those that turn more than yarn_turns[1] times stay; cosines and sines are multiplied by yarn_gain
+            (default 0.1 ln f + 1).  Between them is a ramp, and a model needs the one it was trained with:
+            yarn_ramp "pairs": linear in the pair's index, from the last pair that turns yarn_turns[1] times
+                to the first that turns yarn_turns[0] times or fewer (as released YaRN models have it);
+            yarn_ramp "turns": linear in the number of turns (with yarn_turns=(1, 4), yarn_gain=1 the
+                smoothing between a low and a high frequency factor of 1 and 4).
 
         The angles are computed in float64 and the cosines and sines rounded to float32."""
-        if rotary_dim % 16 or rotary_dim < 16:
-            raise ValueError(f"rotary_dim={rotary_dim} must be a multiple of 16")
-        if linear <= 0 or ntk <= 0 or (yarn is not None and (yarn[0] < 1 or yarn[1] < 1)):
-            raise ValueError(f"linear={linear}, ntk={ntk} must be positive, yarn={yarn} at least (1, 1)")
-        if ntk != 1.0:
-            base = base * ntk ** (rotary_dim / (rotary_dim - 2))
-        half = rotary_dim // 2
-        inv = float(base) ** -(torch.arange(half, dtype=torch.float64) / half) / linear
-        gain = 1.0
-        if yarn is not None:
-            factor, trained = yarn
-            low, high = yarn_turns
-            turns = trained * inv / (2 * math.pi)
-            keep = ((turns - low) / (high - low)).clamp(0, 1)
-            inv = inv * (keep + (1 - keep) / factor)
-            gain = yarn_gain if yarn_gain is not None else 0.1 * math.log(factor) + 1.0
+        inv, gain = _frequencies(rotary_dim, base, linear, ntk, yarn, yarn_turns, yarn_gain, yarn_ramp)
+        if positions < 1:
+            raise ValueError(f"positions={positions} must be at least 1")
         a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv.to(device)
         return cls((torch.stack((a.cos(), a.sin()), -1) * gain).float(), interleaved)
+
+
+def _frequencies(rotary_dim: int, base: float, linear: float, ntk: float, yarn: Optional[Tuple[float, int]],
+                 yarn_turns: Tuple[float, float], yarn_gain: Optional[float], yarn_ramp: str) -> Tuple[torch.Tensor, float]:
+    """The angle per position of each pair (float64 [rotary_dim/2]) and the gain of Rope.make."""
+    if rotary_dim % 16 or rotary_dim < 16:
+        raise ValueError(f"rotary_dim={rotary_dim} must be a multiple of 16")
+    if not base > 1:
+        raise ValueError(f"base={base} must be more than 1")
+    if not (linear > 0 and ntk > 0) or (yarn is not None and not (yarn[0] >= 1 and yarn[1] >= 1)):
+        raise ValueError(f"linear={linear}, ntk={ntk} must be positive, yarn={yarn} at least (1, 1)")
+    if not 0 < yarn_turns[0] < yarn_turns[1]:
+        raise ValueError(f"yarn_turns={yarn_turns} must be positive and rising")
+    if yarn_ramp not in ("pairs", "turns"):
+        raise ValueError(f'yarn_ramp={yarn_ramp!r} must be "pairs" or "turns"')
+    if ntk != 1.0:
+        base = base * ntk ** (rotary_dim / (rotary_dim - 2))
+    half = rotary_dim // 2
+    pair = torch.arange(half, dtype=torch.float64)
+    inv = float(base) ** -(pair / half) / linear
+    if yarn is None:
+        return inv, 1.0
+    factor, trained = yarn
+    low, high = yarn_turns
+    if yarn_ramp == "turns":
+        keep = ((trained * inv / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+    else:
+        def pair_of(turns):  # where, as a real number, a pair would turn that often
+            return half * math.log(trained / linear / (2 * math.pi * turns)) / math.log(base)
+
+        first, last = max(math.floor(pair_of(high)), 0), min(math.ceil(pair_of(low)), rotary_dim - 1)
+        keep = 1 - ((pair - first) / (last - first if last != first else 0.001)).clamp(0, 1)
+    gain = yarn_gain if yarn_gain is not None else 0.1 * math.log(factor) + 1.0
+    return inv * (keep + (1 - keep) / factor), gain
 
 
 class KvCache:
