@@ -119,7 +119,9 @@ exl3_status exl3_cache_read(const exl3_kv_cache *c, const int32_t *slots, int32_
  * offset in cu_q counts as at least those before it and at most tokens; rows
  * that then belong to no sequence are not written.
  *   out = softmax(scale * q k^T) v, products in the cache's dtype with fp32
- * sums, the probabilities rounded to that type for the second product. */
+ * sums, the probabilities rounded to that type for the second product.  out is
+ * either exactly q (same pointer and strides: in place) or does not overlap q;
+ * it never overlaps the cache. */
 exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out, const int32_t *cu_q,
                                  const int32_t *kv_len, const int32_t *page_table, int64_t page_table_stride,
                                  int32_t page_table_width, int32_t batch, int32_t tokens, float scale, int32_t window,
@@ -128,7 +130,8 @@ exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, con
 /* Attention within packed sequences: sequence s is the rows cu[s]..cu[s+1]-1
  * of q, k and v (int32 [batch+1], as cu_q above).  causal: row i sees 0..i of
  * its sequence, else all of it; window > 0 (causal only) the last `window` of
- * those.  k and v have the same heads, q a multiple of them, and token strides
+ * those.  out is exactly q or does not overlap it, as above, and never overlaps
+ * k or v.  k and v have the same heads, q a multiple of them, and token strides
  * of at most 2^22 (the kernels address a tile of keys by 32-bit offsets). */
 exl3_status exl3_prompt_attention(const exl3_rows *q, const exl3_rows *k, const exl3_rows *v, const exl3_rows *out,
                                   const int32_t *cu, int32_t batch, int32_t tokens, int32_t head_dim, int32_t dtype,

@@ -430,7 +430,8 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
     q [tokens, q_heads, head_dim]: sequence s has rows cu_q[s]..cu_q[s+1]-1 (int32 [batch+1]) and kv_len[s] keys
     (int32 [batch]); its last row is at position kv_len[s]-1.  A row sees the keys up to its own position (window > 0:
     the last `window` of them).  page_table int32 [batch, width]: the page of keys j*page_size...; pages that are not
-    the cache's (-1) are holes.  scale defaults to head_dim^-0.5.  Rows that see no key are zero."""
+    the cache's (-1) are holes.  scale defaults to head_dim^-0.5.  Rows that see no key are zero.
+    out may be q (in place), and else overlaps neither it nor the cache."""
     if _current_device() != cache.device.index:
         with torch.cuda.device(cache.device):
             return paged_attention(cache, q, cu_q, kv_len, page_table, scale, window, out)
@@ -458,7 +459,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
                      window: int = 0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention within packed sequences: q [tokens, q_heads, head_dim], k and v [tokens, kv_heads, head_dim], sequence
     s the rows cu_seqlens[s]..cu_seqlens[s+1]-1 (int32 [batch+1]).  causal: a row sees the rows of its sequence up to
-    itself (window > 0: the last `window` of them), else all.  scale defaults to head_dim^-0.5."""
+    itself (window > 0: the last `window` of them), else all.  scale defaults to head_dim^-0.5.  out may be q (in place),
+    and else overlaps none of q, k and v."""
     T, H, D = q.shape
     B = cu_seqlens.shape[0] - 1
     qr, kr, vr = _rows(q, "q"), _rows(k, "k", q), _rows(v, "v", q)

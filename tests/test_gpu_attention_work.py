@@ -111,3 +111,25 @@ def test_padding_rows_leave_the_cache_alone(bits):
         assert same_bits(a[keep], b[keep])
     for i, s in ((0, 17), (1, 72)):
         assert torch.equal(after[1][s].double().cpu(), ref.quantise(y[i].cpu(), bits))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,keys", [(1, 5000), (7, 9000), (200, 700), (150, 6000)])  # few rows and tiles, split and whole
+def test_results_in_place_of_queries(n, keys, d):
+    hq, hkv, page = 8, 2, 64
+    cache = ex.KvCache.empty(-(-keys // page), page, hkv, d)
+    k, v = normal(12, (keys, hkv, d)).cuda(), normal(13, (keys, hkv, d)).cuda()
+    ex.cache_write(cache, k, v, torch.arange(keys, dtype=torch.int32, device="cuda"))
+    table = torch.arange(cache.pages, dtype=torch.int32, device="cuda")[None]
+    qkv = normal(14, (n, (hq + 2 * hkv) * d)).cuda()
+    q, kn, vn = ex.split_heads(qkv, hq, hkv, d)
+    rest = qkv[:, hq * d:].clone()
+    cu = ints([0, n])
+    want = ex.paged_attention(cache, q, cu, ints([keys]), table)
+    want2 = ex.prompt_attention(q, kn, vn, cu)
+    keep = q.clone()
+    assert ex.paged_attention(cache, q, cu, ints([keys]), table, out=q) is q
+    assert same_bits(q, want) and same_bits(qkv[:, hq * d:], rest)
+    q.copy_(keep)
+    ex.prompt_attention(q, kn, vn, cu, out=q)
+    assert same_bits(q, want2) and same_bits(qkv[:, hq * d:], rest)
