@@ -59,13 +59,18 @@ struct Half<false> {
 // moves, and what is summed is scaled, only when some row's grew by more than
 // LAG, so the largest of a row is between 2^LIFT and 2^(LIFT + LAG).  They are
 // rounded to the type for the second product (relative 2^-8 or 2^-11; the sums
-// take them unrounded).  fp16 loses bits below 2^-14 and everything below
-// 2^-25; with LIFT 7 that is 2^-21 and 2^-32 of the row's largest, as low as the
-// type's range (2^15 at most) lets it be.  With 0, 120000 keys of 1.5 * 2^-24 each
-// beside one of 1 weighed 1.42% instead of 1.06%.
+// take them unrounded).
+// fp16 loses bits below 2^-14 and everything below 2^-25; with LIFT 7 that is
+// 2^-21 and 2^-32 of the row's largest, as low as the type's range (2^15 at most)
+// lets it be.  With 0, 120000 keys of 1.5 * 2^-24 each beside one of 1 weighed
+// 1.42% instead of 1.06%.
+// bf16 has fp32's range, and so have its values: what a wave or a part sums
+// before it is joined with the others must not be infinite where the result is
+// not.  With LIFT -24 the largest is 2^-16 at most, so 65536 keys of the largest
+// value fit; what is lost is scores 102 powers of two below the row's largest.
 constexpr float PROB_LAG = 8.f;
 template <bool BF16>
-constexpr float PROB_LIFT = BF16 ? 0.f : 7.f;
+constexpr float PROB_LIFT = BF16 ? -24.f : 7.f;
 
 // What is subtracted from a row's scores, given its running maximum (-inf: no key yet).
 template <bool BF16>
