@@ -121,7 +121,11 @@ exl3_status exl3_cache_read(const exl3_kv_cache *c, const int32_t *slots, int32_
  *   out = softmax(scale * q k^T) v, products in the cache's dtype with fp32
  * sums, the probabilities rounded to that type for the second product.  out is
  * either exactly q (same pointer and strides: in place) or does not overlap q;
- * it never overlaps the cache. */
+ * it never overlaps the cache.
+ *   One kernel, for few rows a sequence or for many, serves the whole call and
+ * is chosen by the average number of new tokens: chunks of a prompt and single
+ * tokens are faster in two calls than together (a chunk of 500 tokens over 20000
+ * keys 243 us, 63 single tokens over up to 8000 keys 120, both in one call 480). */
 exl3_status exl3_paged_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out, const int32_t *cu_q,
                                  const int32_t *kv_len, const int32_t *page_table, int64_t page_table_stride,
                                  int32_t page_table_width, int32_t batch, int32_t tokens, float scale, int32_t window,

@@ -167,13 +167,20 @@ struct AttnPlan {
   size_t workspace;
 };
 
-// Splitting aims at whole rounds of the workgroups that the GPU holds at once
+// Splitting aims at a multiple of a round, one or two workgroups on every CU
 // (find_work).  Few tiles split into equal parts, and one round is best (3
 // sequences of up to 120000 keys, 4 bits, heads of 256: 96 us in one round,
 // 111 in two, 136 in four); tiles of unequal keys need more, smaller parts to
 // even out (64 sequences of up to 16000 keys, 8 bits: 242 us in one round, 190
 // in two, 201 in four; chunks of up to 1000 tokens over 20000 keys on the tile
 // kernel: 890, 803 and 712 us in one, two and four).
+//
+// The workgroups that a round counts on a CU are a choice, not what an
+// instance's registers allow: of the small kernel two fit with heads of 256 at
+// 4 bits, where one is counted, and three with most of the narrower heads,
+// where two are.  Counted as they fit, those calls' times fall by 6 to 12%, but
+// the same rule then gives others twice (heads of 64: 1.5 times) the parts, and
+// those take 5 to 38% more.
 //
 // The least keys of a part: splitting costs the write and the read of a part's
 // sums, 8 KB (heads of 128) in the small kernel, 66 KB in the tile kernel (132
@@ -219,7 +226,7 @@ exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads, int32
   pl->part_min = tile ? TILE_PART_MIN : PART_MIN;
   const int32_t R = tile ? exl3::ATTN_TILE_ROWS : 16 * pl->columns;
   const int64_t tiles = (int64_t)tokens * group / R + batch;  // at most, on each key/value head
-  const int64_t per_cu = (tile ? head_dim == 256 : head_dim * pl->columns >= 256) ? 1 : 2;  // workgroups, by registers
+  const int64_t per_cu = (tile ? head_dim == 256 : head_dim * pl->columns >= 256) ? 1 : 2;  // workgroups of a round
   const int64_t round = per_cu * exl3::host_cus();
   const int64_t rounds = 4 * tiles * kv_heads <= round ? 1 : tile ? 4 : 2;
   const int64_t want = std::max<int64_t>(kv_heads, rounds * round);

@@ -25,11 +25,12 @@
 // waits (lengths, page numbers, rows, the join of waves and of parts).
 // Measured: 64 sequences of up to 16000 keys, 8 bits, 32/8 heads of 128, 957
 // MB in 177 us, 5.4 TB/s (a streaming read reaches 5.73 here); 3 sequences of
-// up to 120000 keys, 4 bits, 24/4 heads of 256, 293 MB in 76 us, 3.9 TB/s (one
-// workgroup a CU: with two this takes 12% less, but 24 sequences of 8000 keys
-// 38% more; a 4-bit key costs the same vector work for half the bytes); 24
-// sequences of up to 7 tokens over windows of 4096 keys, 64/8 heads of 64, 131
-// MB in 41 us, 3.2 TB/s (two columns of products and exponentials to a load);
+// up to 120000 keys, 4 bits, 24/4 heads of 256, 293 MB in 76 us, 3.9 TB/s (split
+// for one workgroup a CU though two fit, and a 4-bit key costs the same vector
+// work for half the bytes; split for two, this takes 12% less, but 24 sequences
+// of 8000 keys, which then have twice the parts, 38% more); 24 sequences of up
+// to 7 tokens over windows of 4096 keys, 64/8 heads of 64, 131 MB in 41 us, 3.2
+// TB/s (two columns of products and exponentials to a load);
 // one token over 1100 keys, 4.5 MB in 8.9 us.
 #pragma once
 

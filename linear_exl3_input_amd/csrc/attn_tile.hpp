@@ -35,15 +35,19 @@
 // What bounds it: vector work about as long as the products, on the same
 // SIMDs.  A wave-tile is 32 products of 32x32x16 (1024 cycles of its SIMD's
 // matrix unit), some 1060 cycles of vector work, half of them exponentials,
-// and 32 KB of LDS reads; counters show the matrix units busy for 48% of the
-// cycles, the vector units for 50%, the LDS for 36%.  Measured: prompts of up
-// to 8000 tokens, 32/8 heads of 128, 931 GFLOP in 960 us, 970 TFLOP/s (a large
-// matrix product reaches 1283 here); chunks of up to 1000 tokens over up to
-// 20000 keys of 8 bits, 523 GFLOP in 670 us, 780; windows of 2048, 24/4 heads
-// of 256, 206 GFLOP in 278 us, 743 (one wave a SIMD, as o alone takes 128
-// registers).  64 rows a wave halve the LDS reads but spill; eight waves as
-// two groups of four that alternate products and vector work take 925 us on
-// the first but more on chunks, and spill with heads of 256.
+// and 32 KB of LDS reads; counters show the matrix units busy for 47% of the
+// cycles, the vector units for 52%, the LDS for 37%.  Measured (cards differ by
+// up to 10% here): prompts of up to 8000 tokens, 32/8 heads of 128, 931 GFLOP in
+// 960-1050 us, 890-970 TFLOP/s (a large matrix product reaches 1283 on the
+// fastest); chunks of up to 1000 tokens over up to 20000 keys of 8 bits, 523
+// GFLOP in 690-735 us, 710-760; windows of 2048, 24/4 heads of 256, 206 GFLOP in
+// 277-295 us, 700-745 (one wave a SIMD, as o alone takes 128 registers).
+// Registers are short: two waves a SIMD have 256 each, which heads of 64 and
+// 128 fill; over codes and with heads of 64 over 16-bit caches 1 to 14 registers
+// are kept in memory, elsewhere none.  64 rows a wave halve the LDS reads but
+// do not fit; eight waves as two groups of four that alternate products and
+// vector work took 925 us on the first (where this took 960) but more on chunks,
+// and do not fit with heads of 256.
 #pragma once
 
 #include "attn_small.hpp"
