@@ -1,0 +1,79 @@
+/*
+ * exl3_step.h -- C ABI of a serving step's operators beside those of
+ * exl3_attn.h: block tables and slot maps from request lengths, the rotation
+ * with norms of each query and key head and with several position axes,
+ * attention with first tokens that stay visible beside a window, and
+ * attention of sequences that share a prefix.  Same library, conventions
+ * (streams, workspaces, checks before any HIP call, values in device memory
+ * that are out of range), status codes and error text as exl3_attn.h.
+ */
+#ifndef EXL3_STEP_H
+#define EXL3_STEP_H
+
+#include "exl3_attn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Rotary positions of several axes (time, height and width of a video's
+ * patches): pair i turns by the angle that the table has for the token's
+ * position on axis (axis_of[i / 16] >> 2 * (i % 16)) & 3, which is below axes.
+ * positions are int32 [axes][tokens], rows axis_stride apart; one outside
+ * 0..rotary.positions-1 gives NaN in the pairs of its axis. */
+typedef struct exl3_rotary_axes {
+  exl3_rotary rotary;
+  int32_t axes;        /* 1..4 */
+  uint32_t axis_of[8]; /* two bits a pair */
+} exl3_rotary_axes;
+
+/* Norms of each query and key head, before the rotation:
+ *   n = x / sqrt(mean(x^2) + eps) * w
+ * over the head's values.  w fp32: head_dim weights for all heads, or one such
+ * row for each (q_rows, k_rows: 1 or the number of heads). */
+typedef struct exl3_head_norm {
+  const float *q, *k;
+  int32_t q_rows, k_rows;
+  float eps; /* 1e-30 .. 1 */
+} exl3_head_norm;
+
+/* exl3_rope with norms (n may be NULL: none) and axes: norm, rotation and one
+ * rounding to the type, everything before it in fp32. */
+exl3_status exl3_norm_rope(const exl3_rotary_axes *r, const exl3_head_norm *n, const int32_t *positions,
+                           int64_t axis_stride, int32_t tokens, int32_t head_dim, int32_t dtype, const exl3_rows *q,
+                           const exl3_rows *q_out, const exl3_rows *k, const exl3_rows *k_out, void *stream);
+
+/* exl3_rope_cache_write with norms and axes; the same bits as exl3_norm_rope
+ * and exl3_cache_write of its k_out. */
+exl3_status exl3_norm_rope_cache_write(const exl3_kv_cache *c, const exl3_rotary_axes *r, const exl3_head_norm *n,
+                                       const int32_t *positions, int64_t axis_stride, const int32_t *slots,
+                                       int32_t tokens, const exl3_rows *q, const exl3_rows *q_out, const exl3_rows *k,
+                                       const exl3_rows *k_out, const exl3_rows *v, void *stream);
+
+/* What a step needs of its requests' lengths, in one launch.  Request b has
+ * kv_len[b] tokens in a cache of `pages` pages of page_size tokens, on the pages
+ * page_table[b][0..], and wants q_len[b] more.  The step has room for `tokens`
+ * rows, which the requests get in order:
+ *   cu_q [batch+1]   request b's rows are cu_q[b] .. cu_q[b+1]-1 (a request that
+ *                    finds less room than it wants gets what is left)
+ *   kv_out [batch]   kv_len and the new rows
+ *   positions, slots [tokens]   of each row; rows that no request has: 0 and -1
+ *   page_table       entries ceil(kv_len/page_size) .. ceil(kv_out/page_size)-1
+ *                    (below width) become free_pages[taken], [taken+1], ... in the
+ *                    order of the requests, -1 past n_free; other entries stay
+ *   counts [2]       the rows that the requests wanted in all (at most 2^31-1), and the
+ *                    entries that the table needed
+ * taken: NULL (0) or one int32, the free pages used by earlier steps.  A row
+ * whose page is not one of the cache's has slot -1.  q_len counts as 0..2^20,
+ * kv_len as 0..2^30, taken as 0..n_free.  Outputs overlap neither inputs nor
+ * each other; page_table is in both. */
+exl3_status exl3_cache_extend(int32_t pages, int32_t page_size, const int32_t *q_len, const int32_t *kv_len,
+                              int32_t batch, int32_t *page_table, int64_t page_table_stride, int32_t page_table_width,
+                              const int32_t *free_pages, int32_t n_free, const int32_t *taken, int32_t tokens,
+                              int32_t *cu_q, int32_t *kv_out, int32_t *positions, int32_t *slots, int32_t *counts,
+                              void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* EXL3_STEP_H */

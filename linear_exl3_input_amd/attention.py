@@ -1,18 +1,23 @@
 """What stands between a decoder's q/k/v and output projections on an MI355X:
-rotary positions, a paged key/value cache that is quantized as it is written,
-attention over that cache and attention over packed prompts.
+rotary positions (with norms of the heads, over several axes), a paged key/value
+cache that is quantized as it is written, its page tables and slots from the
+requests' lengths, attention over that cache (of sequences that share a prefix
+too) and attention over packed prompts.
 
-A ctypes binding over ``include/exl3_attn.h`` like the package's own: tensor
-metadata is checked here, everything else by the library, and there is no
-fallback.  One decoder layer's step of a server:
+A ctypes binding over ``include/exl3_attn.h`` and ``include/exl3_step.h`` like
+the package's own: tensor metadata is checked here, everything else by the
+library, and there is no fallback.  One decoder layer's step of a server:
 
-    rope = Rope.make(head_dim, rotary_dim, base=1e6, positions=32768)
+    rope = Rope.make(rotary_dim, base=1e6, positions=32768)
+    norm = HeadNorm(q_weight, k_weight)
     cache = KvCache.empty(pages, page_size, kv_heads, head_dim, bits=8)
+    ...
+    step = cache_extend(cache, q_len, kv_len, page_table, free_pages, tokens)
     ...
     qkv = forward(w_qkv, x)                       # [tokens, (hq + 2*hkv)*d]
     q, k, v = split_heads(qkv, hq, hkv, head_dim)      # views
-    q = rope_cache_write(cache, rope, positions, slots, q, k, v)
-    y = paged_attention(cache, q, cu_q, kv_len, page_table)
+    q = rope_cache_write(cache, rope, step.positions, step.slots, q, k, v, norm=norm)
+    y = paged_attention(cache, q, step.cu_q, step.kv_len, page_table)
     x = forward(w_o, y.view(tokens, -1))
 
 Rows may have any token and head stride (a multiple of 8 values), so the
@@ -26,16 +31,17 @@ import ctypes
 import math
 import os
 import re
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
 from . import _BF16, _F16, _HERE, _check, _workspace, _workspaces, _ws_needs_zero, load
 
 __all__ = ["Rope", "KvCache", "split_heads", "rope", "cache_write", "cache_read", "rope_cache_write",
-           "paged_attention", "prompt_attention", "attention_workspace_bytes"]
+           "paged_attention", "prompt_attention", "attention_workspace_bytes", "HeadNorm", "CacheStep", "cache_extend"]
 
 ATTN_HEADER = os.path.join(os.path.dirname(_HERE), "include", "exl3_attn.h")
+STEP_HEADER = os.path.join(os.path.dirname(_HERE), "include", "exl3_step.h")
 HEAD_DIMS = (64, 128, 256)
 
 
@@ -47,6 +53,15 @@ class _Rows(ctypes.Structure):
 class _Rotary(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int32), ("rot", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32)]
+
+
+class _RotaryAxes(ctypes.Structure):
+    _fields_ = [("rotary", _Rotary), ("axes", ctypes.c_int32), ("axis_of", ctypes.c_uint32 * 8)]
+
+
+class _HeadNorm(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_rows", ctypes.c_int32), ("k_rows", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 class _Cache(ctypes.Structure):
@@ -66,6 +81,7 @@ def _lib():
         L = load()
         vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         R, T, C = ctypes.POINTER(_Rows), ctypes.POINTER(_Rotary), ctypes.POINTER(_Cache)
+        A, N = ctypes.POINTER(_RotaryAxes), ctypes.POINTER(_HeadNorm)
         sig = {
             "exl3_rope": (i32, [T, vp, i32, i32, i32, R, R, R, R, vp]),
             "exl3_cache_write": (i32, [C, R, R, vp, i32, vp]),
@@ -74,6 +90,9 @@ def _lib():
             "exl3_paged_attention": (i32, [C, R, R, vp, vp, vp, i64, i32, i32, i32, f32, i32, vp, sz, vp]),
             "exl3_prompt_attention": (i32, [R, R, R, R, vp, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp]),
             "exl3_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+            "exl3_norm_rope": (i32, [A, N, vp, i64, i32, i32, i32, R, R, R, R, vp]),
+            "exl3_norm_rope_cache_write": (i32, [C, A, N, vp, i64, vp, i32, R, R, R, R, R, vp]),
+            "exl3_cache_extend": (i32, [i32, i32, vp, vp, i32, vp, i64, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -83,9 +102,9 @@ def _lib():
     return _fns
 
 
-def attn_header_symbols() -> Tuple[str, ...]:
-    """Every function that exl3_attn.h declares."""
-    text = re.sub(r"/\*.*?\*/", "", open(ATTN_HEADER).read(), flags=re.S)
+def attn_header_symbols(header: str = ATTN_HEADER) -> Tuple[str, ...]:
+    """Every function that exl3_attn.h (or another header) declares."""
+    text = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
     return tuple(sorted(set(re.findall(r"\b(exl3_[a-z_]+)\s*\(", text))))
 
 
@@ -182,9 +201,13 @@ class Rope:
     """A table of rotations, float32 [positions, rotary_dim/2, 2] (cosine, sine).
 
     interleaved False pairs value i with i + rotary_dim/2, True 2i with 2i + 1;
-    values from rotary_dim on stay as they are."""
+    values from rotary_dim on stay as they are.
 
-    def __init__(self, table: torch.Tensor, interleaved: bool = False):
+    axes: the axis (0..3) whose position turns each pair, for tokens that have several (time, height
+    and width of a video's patches); positions are then int32 [number of axes, tokens].  None: one axis,
+    positions [tokens]."""
+
+    def __init__(self, table: torch.Tensor, interleaved: bool = False, axes: Optional[Sequence[int]] = None):
         if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
             raise ValueError("table must be a contiguous float32 tensor [positions, rotary_dim/2, 2]")
         if not table.is_cuda:
@@ -193,11 +216,15 @@ class Rope:
         self.positions, self.rotary_dim = table.shape[0], 2 * table.shape[1]
         self._view = _Rotary(table.data_ptr(), self.positions, self.rotary_dim, int(self.interleaved))
         self._ref = ctypes.byref(self._view)
+        self.axes, self.n_axes, words = _axes(axes, self.rotary_dim)
+        self._axes_view = _RotaryAxes(self._view, self.n_axes, words)
+        self._axes_ref = ctypes.byref(self._axes_view)
 
     @classmethod
     def make(cls, rotary_dim: int, base: float, positions: int, interleaved: bool = False, linear: float = 1.0,
              ntk: float = 1.0, yarn: Optional[Tuple[float, int]] = None, yarn_turns: Tuple[float, float] = (1.0, 32.0),
-             yarn_gain: Optional[float] = None, yarn_ramp: str = "pairs", device="cuda") -> "Rope":
+             yarn_gain: Optional[float] = None, yarn_ramp: str = "pairs", device="cuda",
+             sections: Optional[Sequence[int]] = None, in_turn: bool = False) -> "Rope":
         """Frequencies base^(-2i/rotary_dim), stretched for contexts longer than trained:
 
         linear f: every position is divided by f.
@@ -211,12 +238,39 @@ class Rope:
             yarn_ramp "turns": linear in the number of turns (with yarn_turns=(1, 4), yarn_gain=1 the
                 smoothing between a low and a high frequency factor of 1 and 4).
 
+        sections: the pairs that each of several axes turns, rotary_dim/2 in all: the first sections[0] pairs by
+        axis 0, the next sections[1] by axis 1 and so on; in_turn: pair i by axis i % len(sections) as long as that
+        axis has pairs left, and by axis 0 after that.
+
         The angles are computed in float64 and the cosines and sines rounded to float32."""
+        axes = None if sections is None else _axes_of_sections(sections, rotary_dim, in_turn)
         inv, gain = _frequencies(rotary_dim, base, linear, ntk, yarn, yarn_turns, yarn_gain, yarn_ramp)
         if positions < 1:
             raise ValueError(f"positions={positions} must be at least 1")
         a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv.to(device)
-        return cls((torch.stack((a.cos(), a.sin()), -1) * gain).float(), interleaved)
+        return cls((torch.stack((a.cos(), a.sin()), -1) * gain).float(), interleaved, axes)
+
+
+def _axes(axes: Optional[Sequence[int]], rotary_dim: int):
+    """(axes, their number, two bits a pair for the library)."""
+    words = (ctypes.c_uint32 * 8)()
+    if axes is None:
+        return None, 1, words
+    axes = tuple(int(a) for a in axes)
+    if len(axes) != rotary_dim // 2 or not all(0 <= a <= 3 for a in axes):
+        raise ValueError(f"axes={axes} must name an axis 0..3 for each of {rotary_dim // 2} pairs")
+    for i, a in enumerate(axes[:128]):
+        words[i // 16] |= a << 2 * (i % 16)
+    return axes, max(axes) + 1, words
+
+
+def _axes_of_sections(sections: Sequence[int], rotary_dim: int, in_turn: bool) -> Tuple[int, ...]:
+    n = len(sections)
+    if not 1 <= n <= 4 or min(sections) < 1 or sum(sections) != rotary_dim // 2:
+        raise ValueError(f"sections={tuple(sections)} must be 1 to 4 numbers of pairs, {rotary_dim // 2} in all")
+    if in_turn:
+        return tuple(i % n if i // n < sections[i % n] else 0 for i in range(rotary_dim // 2))
+    return tuple(a for a, pairs in enumerate(sections) for _ in range(pairs))
 
 
 def _frequencies(rotary_dim: int, base: float, linear: float, ntk: float, yarn: Optional[Tuple[float, int]],
@@ -251,6 +305,38 @@ def _frequencies(rotary_dim: int, base: float, linear: float, ntk: float, yarn: 
         keep = 1 - ((pair - first) / (last - first if last != first else 0.001)).clamp(0, 1)
     gain = yarn_gain if yarn_gain is not None else 0.1 * math.log(factor) + 1.0
     return inv * (keep + (1 - keep) / factor), gain
+
+
+class HeadNorm:
+    """Norms of each query and key head before the rotation: x / sqrt(mean(x^2) + eps) * weight over the head's
+    values, in float32 up to the rounding after the rotation.
+
+    q_weight, k_weight [head_dim], or [heads, head_dim] for weights of each head's own; copied as float32, plus one
+    with one_plus (weights that are kept as their distance from one).  k_weight None: only q is given to the calls."""
+
+    def __init__(self, q_weight: torch.Tensor, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 one_plus: bool = False):
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is None:
+                continue
+            if w.dim() not in (1, 2) or w.shape[-1] not in HEAD_DIMS or w.shape[0] == 0 or not w.is_floating_point():
+                raise ValueError(f"{name} is {w.dtype} {tuple(w.shape)}, expected floating [64, 128 or 256] or "
+                                 "[heads, 64, 128 or 256]")
+            if not w.is_cuda:
+                raise ValueError(f"{name} must be a GPU tensor")
+            if w.device != q_weight.device or w.shape[-1] != q_weight.shape[-1]:
+                raise ValueError(f"{name} is {tuple(w.shape)} on {w.device}, q_weight {tuple(q_weight.shape)} on "
+                                 f"{q_weight.device}")
+        if not 1e-30 <= eps <= 1:
+            raise ValueError(f"eps={eps} must be 1e-30..1")
+        self.eps, self.head_dim, self.device = float(eps), q_weight.shape[-1], q_weight.device
+        # (a copy always: the caller may write to its tensors)
+        self.q_weight, self.k_weight = (None if w is None else (w.detach().float() + (1.0 if one_plus else 0.0)).contiguous()
+                                        for w in (q_weight, k_weight))
+        rows = lambda w: 0 if w is None else 1 if w.dim() == 1 else w.shape[0]  # noqa: E731
+        self._view = _HeadNorm(self.q_weight.data_ptr(), None if k_weight is None else self.k_weight.data_ptr(),
+                               rows(q_weight), rows(k_weight), self.eps)
+        self._ref = ctypes.byref(self._view)
 
 
 class KvCache:
@@ -329,16 +415,35 @@ class KvCache:
         return torch.where(missing, -1, slot).int()
 
 
+def _positions(r: Rope, positions: torch.Tensor, tokens: int, device) -> Tuple[int, int]:
+    """The address and the axes' stride of positions [tokens], or [axes, tokens] for rotations of several axes."""
+    if r.axes is None:
+        return _ints(positions, "positions", tokens, device), 0
+    if (positions.dtype != torch.int32 or positions.device != device or positions.dim() != 2 or
+            positions.shape[0] != r.n_axes or positions.shape[1] != tokens or (tokens > 1 and positions.stride(1) != 1)):
+        raise ValueError(f"positions must be int32 [{r.n_axes}, {tokens}] with dense rows on {device}, got "
+                         f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
+    return positions.data_ptr(), positions.stride(0) if r.n_axes > 1 else 0
+
+
+def _norm(norm: Optional[HeadNorm], q: torch.Tensor):
+    if norm is None:
+        return None
+    if norm.device != q.device or norm.head_dim != q.shape[2]:
+        raise ValueError(f"the norms are of {norm.head_dim}-value heads on {norm.device}, q has {q.shape[2]} on {q.device}")
+    return norm._ref
+
+
 def rope(r: Rope, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Tensor] = None,
-         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, norm: Optional[HeadNorm] = None):
     """Rotates q [tokens, heads, head_dim] (and k) by their positions in one launch; returns q_out, or (q_out, k_out).
-    An output may be its input (in place)."""
+    An output may be its input (in place).  norm: the heads are normed first, in the same pass."""
     T, _, D = q.shape
     qr = _rows(q, "q")
     _same_device(r, q)
     if _current_device() != q.device.index:
         with torch.cuda.device(q.device):
-            return rope(r, positions, q, k, q_out, k_out)
+            return rope(r, positions, q, k, q_out, k_out, norm)
     q_out, qo = _out(q_out, q, "q_out")
     kr = ko = None
     if k is not None:
@@ -347,6 +452,11 @@ def rope(r: Rope, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Te
         ko = ctypes.byref(ko)
     elif k_out is not None:
         raise ValueError("k_out without k")
+    if norm is not None or r.axes is not None:
+        at, stride = _positions(r, positions, T, q.device)
+        _check(_lib().exl3_norm_rope(r._axes_ref, _norm(norm, q), at, stride, T, D, _dtype_id(q.dtype, "q"),
+                                     ctypes.byref(qr), ctypes.byref(qo), kr, ko, _raw_stream(q.device.index)))
+        return q_out if k is None else (q_out, k_out)
     _check(_lib().exl3_rope(r._ref, _ints(positions, "positions", T, q.device), T, D, _dtype_id(q.dtype, "q"),
                             ctypes.byref(qr), ctypes.byref(qo), kr, ko, _raw_stream(q.device.index)))
     return q_out if k is None else (q_out, k_out)
@@ -374,12 +484,12 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
 
 def rope_cache_write(cache: KvCache, r: Rope, positions: torch.Tensor, slots: torch.Tensor, q: torch.Tensor,
                      k: torch.Tensor, v: torch.Tensor, q_out: Optional[torch.Tensor] = None,
-                     k_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     k_out: Optional[torch.Tensor] = None, norm: Optional[HeadNorm] = None) -> torch.Tensor:
     """rope(q, k) and cache_write(rotated k, v) in one launch, with the same bits; returns the rotated q.  The rotated
-    k also goes to k_out when that is given."""
+    k also goes to k_out when that is given.  norm: q and k are normed per head first, in the same pass."""
     if _current_device() != cache.device.index:
         with torch.cuda.device(cache.device):
-            return rope_cache_write(cache, r, positions, slots, q, k, v, q_out, k_out)
+            return rope_cache_write(cache, r, positions, slots, q, k, v, q_out, k_out, norm)
     T = q.shape[0]
     qr, kr, vr = _cache_rows(cache, q, "q"), _cache_rows(cache, k, "k"), _cache_rows(cache, v, "v")
     if k.shape[0] != T or v.shape[0] != T:
@@ -387,6 +497,12 @@ def rope_cache_write(cache: KvCache, r: Rope, positions: torch.Tensor, slots: to
     _same_device(r, q)
     q_out, qo = _out(q_out, q, "q_out")
     ko = ctypes.byref(_out(k_out, k, "k_out")[1]) if k_out is not None else None
+    if norm is not None or r.axes is not None:
+        at, stride = _positions(r, positions, T, q.device)
+        _check(_lib().exl3_norm_rope_cache_write(cache._ref, r._axes_ref, _norm(norm, q), at, stride,
+                                                 _ints(slots, "slots", T, q.device), T, ctypes.byref(qr), ctypes.byref(qo),
+                                                 ctypes.byref(kr), ko, ctypes.byref(vr), _raw_stream(cache.device.index)))
+        return q_out
     _check(_lib().exl3_rope_cache_write(cache._ref, r._ref, _ints(positions, "positions", T, q.device),
                                         _ints(slots, "slots", T, q.device), T, ctypes.byref(qr), ctypes.byref(qo),
                                         ctypes.byref(kr), ko, ctypes.byref(vr), _raw_stream(cache.device.index)))
@@ -439,10 +555,7 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
     B = kv_len.shape[0]
     dev = cache.device
     qr = _cache_rows(cache, q, "q")
-    if (page_table.dtype != torch.int32 or page_table.device != dev or page_table.dim() != 2 or
-            page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        raise ValueError(f"page_table must be int32 [{B}, width] with dense rows on {dev}, got {page_table.dtype} "
-                         f"{tuple(page_table.shape)}")
+    _page_table(page_table, B, dev)
     out, o = _out(out, q, "out")
     L = _lib()
     need = L.exl3_attention_workspace_bytes(B, T, H, cache.heads, D)
@@ -475,4 +588,55 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     _check(L.exl3_prompt_attention(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(o),
                                    _ints(cu_seqlens, "cu_seqlens", B + 1, q.device), B, T, D, _dtype_id(q.dtype, "q"),
                                    int(causal), _window(window), D ** -0.5 if scale is None else scale, ws, wsn, stream))
+    return out
+
+
+class CacheStep(NamedTuple):
+    """A step's rows of requests over the cache, int32 on the GPU (cache_extend)."""
+
+    cu_q: torch.Tensor       # [batch+1] request b's rows are cu_q[b]..cu_q[b+1]-1
+    kv_len: torch.Tensor     # [batch] tokens in the cache with the step's own
+    positions: torch.Tensor  # [tokens] of each row (0 where no request has it)
+    slots: torch.Tensor      # [tokens] in the cache (-1 where there is none)
+    counts: torch.Tensor     # [2] the rows that were wanted, and the pages that were needed
+
+
+def _page_table(page_table: torch.Tensor, batch: int, device) -> None:
+    if (page_table.dtype != torch.int32 or page_table.device != device or page_table.dim() != 2 or
+            page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError(f"page_table must be int32 [{batch}, width] with dense rows on {device}, got {page_table.dtype} "
+                         f"{tuple(page_table.shape)}")
+
+
+def cache_extend(cache: KvCache, q_len: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                 free_pages: torch.Tensor, tokens: int, taken: Optional[torch.Tensor] = None,
+                 out: Optional[CacheStep] = None) -> CacheStep:
+    """What a step needs of its requests' lengths, in one launch that reads nothing back: request b has kv_len[b] tokens
+    in the cache and wants q_len[b] more (int32 [batch]), of `tokens` rows that the requests get in order.
+
+    page_table (int32 [batch, width]) gets the pages that the new tokens need, from free_pages (int32 [n]) in the
+    requests' order, from place taken[0] on (int32 [1]; None: from the first); -1 where none is left.  Returns the rows'
+    offsets, the new lengths, and each row's position and slot, in new tensors or those of `out`, which overlap no input;
+    counts[1] is what the step took of free_pages, or more if they were too few.  Rows that no request has (a step of
+    fixed size) have slot -1, and so do those without a page.  A request that wants more rows than are left gets those:
+    counts[0] is then more than `tokens`."""
+    dev = cache.device
+    if _current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return cache_extend(cache, q_len, kv_len, page_table, free_pages, tokens, taken, out)
+    B = kv_len.shape[0]
+    _page_table(page_table, B, dev)
+    if not 0 <= tokens <= 1 << 20:
+        raise ValueError(f"tokens={tokens}, must be 0 to {1 << 20}")
+    at = [_ints(q_len, "q_len", B, dev), _ints(kv_len, "kv_len", B, dev)]
+    free_at = _ints(free_pages, "free_pages", free_pages.shape[0], dev)
+    taken_at = None if taken is None else _ints(taken, "taken", 1, dev)
+    if out is None:
+        # views of one new tensor
+        out = CacheStep(*kv_len.new_empty(2 * B + 1 + 2 * tokens + 2).split((B + 1, B, tokens, tokens, 2)))
+    made = [_ints(t, f"out.{name}", n, dev) for t, name, n in
+            zip(out, CacheStep._fields, (B + 1, B, tokens, tokens, 2))]
+    _check(_lib().exl3_cache_extend(cache.pages, cache.page_size, *at, B, page_table.data_ptr(), page_table.stride(0),
+                                    page_table.shape[1], free_at, free_pages.shape[0], taken_at, tokens, *made,
+                                    _raw_stream(dev.index)))
     return out

@@ -57,6 +57,18 @@ struct RowsParams {
   CacheView cache;
 };
 
+// Rows of a launch whose queries and keys are normed per head before they are
+// rotated, or whose pairs turn by several axes' positions, or both.
+struct NormRowsParams {
+  RowsParams rows;           // positions: [axes][tokens], axis_stride apart
+  int64_t axis_stride;
+  uint32_t axis_of[8];       // the axis of each pair, two bits each
+  int32_t axes;
+  const float *wq, *wk;      // null: not normed; weights of the heads' dims
+  int32_t wq_step, wk_step;  // from one head's weights to the next's: 0 or the head size
+  float eps;
+};
+
 struct ReadParams {
   Rows k_out, v_out;
   const int32_t *slots;
@@ -91,6 +103,7 @@ struct AttnParams {
 
 // bits: 0 (no cache), 16, 8, 4.
 hipError_t launch_rows(int head_dim, bool bf16, int bits, const RowsParams &p, hipStream_t s);
+hipError_t launch_norm_rows(int head_dim, bool bf16, int bits, const NormRowsParams &p, hipStream_t s);
 hipError_t launch_cache_read(int head_dim, bool bf16, int bits, const ReadParams &p, hipStream_t s);
 
 // Tiles of 16 * columns query rows, one workgroup each (columns 1, or 2 for heads of 64 and 128).

@@ -1,0 +1,204 @@
+// Host side of the C ABI declared in include/exl3_step.h: argument checks and
+// launches.  Every check runs before any HIP call.
+#include "../../include/exl3_step.h"
+#include "attn_checks.hpp"
+#include "step_launch.hpp"
+
+namespace {
+
+using namespace exl3;
+
+exl3_status check_axes(const exl3_rotary_axes *r, const int32_t *positions, int64_t axis_stride, int32_t tokens,
+                       int32_t head_dim) {
+  if (r == nullptr) return host_fail(EXL3_ERR_INVALID_ARG, "rotary is NULL");
+  exl3_status st;
+  if ((st = check_rotary(&r->rotary, positions, tokens, head_dim)) != EXL3_OK) return st;
+  if (r->axes < 1 || r->axes > 4) return host_fail(EXL3_ERR_INVALID_ARG, "axes=%d, must be 1..4", r->axes);
+  for (int i = 0; i < r->rotary.rot / 2; ++i) {
+    const int a = (int)((r->axis_of[i / 16] >> (2 * (i % 16))) & 3u);
+    if (a >= r->axes) return host_fail(EXL3_ERR_INVALID_ARG, "pair %d turns by axis %d of %d", i, a, r->axes);
+  }
+  if (axis_stride < 0 || axis_stride > (1ll << 40))
+    return host_fail(EXL3_ERR_INVALID_ARG, "axis_stride=%lld, must be 0..2^40", (long long)axis_stride);
+  return EXL3_OK;
+}
+
+exl3_status check_norm(const exl3_head_norm *n, const exl3_rows *q, const exl3_rows *k) {
+  if (n == nullptr) return EXL3_OK;
+  exl3_status st;
+  if ((st = check_ptr(n->q, "norm q")) != EXL3_OK) return st;
+  if (n->q_rows != 1 && n->q_rows != q->heads)
+    return host_fail(EXL3_ERR_INVALID_ARG, "norm has weights of %d query heads, q has %d", n->q_rows, q->heads);
+  if (k != nullptr) {
+    if ((st = check_ptr(n->k, "norm k")) != EXL3_OK) return st;
+    if (n->k_rows != 1 && n->k_rows != k->heads)
+      return host_fail(EXL3_ERR_INVALID_ARG, "norm has weights of %d key heads, k has %d", n->k_rows, k->heads);
+  }
+  if (!(n->eps >= 1e-30f && n->eps <= 1.f))
+    return host_fail(EXL3_ERR_INVALID_ARG, "eps=%g, must be 1e-30..1", (double)n->eps);
+  return EXL3_OK;
+}
+
+NormRowsParams norm_rows(const exl3_rotary_axes *r, const exl3_head_norm *n, const int32_t *positions,
+                         int64_t axis_stride, int32_t tokens, int32_t head_dim, const exl3_rows *q,
+                         const exl3_rows *q_out, const exl3_rows *k, const exl3_rows *k_out) {
+  NormRowsParams p;
+  std::memset(&p, 0, sizeof p);
+  p.rows.q = rows_of(q);
+  p.rows.q_out = rows_of(q_out);
+  p.rows.hq = q->heads;
+  if (k != nullptr) {
+    p.rows.k = rows_of(k);
+    p.rows.hk = k->heads;
+  }
+  if (k_out != nullptr) p.rows.k_out = rows_of(k_out);
+  p.rows.table = r->rotary.table;
+  p.rows.positions = positions;
+  p.rows.n_positions = r->rotary.positions;
+  p.rows.rot = r->rotary.rot;
+  p.rows.interleaved = r->rotary.interleaved;
+  p.rows.tokens = tokens;
+  p.axis_stride = axis_stride;
+  std::memcpy(p.axis_of, r->axis_of, sizeof p.axis_of);
+  p.axes = r->axes;
+  if (n != nullptr) {
+    p.wq = n->q;
+    p.wk = n->k;
+    p.wq_step = n->q_rows > 1 ? head_dim : 0;
+    p.wk_step = n->k_rows > 1 ? head_dim : 0;
+    p.eps = n->eps;
+  }
+  return p;
+}
+
+bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {  // ranges of int32
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an > 0 && bn > 0 && a != nullptr && b != nullptr && x < y + 4 * (uintptr_t)bn && y < x + 4 * (uintptr_t)an;
+}
+
+}  // namespace
+
+extern "C" {
+
+exl3_status exl3_norm_rope(const exl3_rotary_axes *r, const exl3_head_norm *n, const int32_t *positions,
+                           int64_t axis_stride, int32_t tokens, int32_t head_dim, int32_t dtype, const exl3_rows *q,
+                           const exl3_rows *q_out, const exl3_rows *k, const exl3_rows *k_out, void *stream) {
+  host_clear_error();
+  exl3_status st;
+  if ((st = check_shape(tokens, head_dim, dtype)) != EXL3_OK) return st;
+  if ((st = check_axes(r, positions, axis_stride, tokens, head_dim)) != EXL3_OK) return st;
+  if ((st = check_rows(q, "q", tokens, head_dim, false)) != EXL3_OK) return st;
+  if ((st = check_rows(q_out, "q_out", tokens, head_dim, true)) != EXL3_OK) return st;
+  if ((st = check_in_place(q, q_out, "q_out")) != EXL3_OK) return st;
+  if ((k == nullptr) != (k_out == nullptr))
+    return host_fail(EXL3_ERR_INVALID_ARG, "k and k_out must be given together");
+  if (k != nullptr) {
+    if ((st = check_rows(k, "k", tokens, head_dim, false)) != EXL3_OK) return st;
+    if ((st = check_rows(k_out, "k_out", tokens, head_dim, true)) != EXL3_OK) return st;
+    if ((st = check_in_place(k, k_out, "k_out")) != EXL3_OK) return st;
+  }
+  if ((st = check_norm(n, q, k)) != EXL3_OK) return st;
+  if ((st = check_launch_rows(tokens, q->heads + (k ? k->heads : 0))) != EXL3_OK) return st;
+  if (tokens == 0) return EXL3_OK;
+  const NormRowsParams p = norm_rows(r, n, positions, axis_stride, tokens, head_dim, q, q_out, k, k_out);
+  return launched(launch_norm_rows(head_dim, dtype == EXL3_BF16, 0, p, (hipStream_t)stream), "norm and rope launch");
+}
+
+exl3_status exl3_norm_rope_cache_write(const exl3_kv_cache *c, const exl3_rotary_axes *r, const exl3_head_norm *n,
+                                       const int32_t *positions, int64_t axis_stride, const int32_t *slots,
+                                       int32_t tokens, const exl3_rows *q, const exl3_rows *q_out, const exl3_rows *k,
+                                       const exl3_rows *k_out, const exl3_rows *v, void *stream) {
+  host_clear_error();
+  exl3_status st;
+  if ((st = check_cache(c)) != EXL3_OK) return st;
+  const int32_t D = c->head_dim;
+  if ((st = check_shape(tokens, D, c->dtype)) != EXL3_OK) return st;
+  if ((st = check_axes(r, positions, axis_stride, tokens, D)) != EXL3_OK) return st;
+  if ((st = check_rows(q, "q", tokens, D, false)) != EXL3_OK) return st;
+  if ((st = check_rows(q_out, "q_out", tokens, D, true)) != EXL3_OK) return st;
+  if ((st = check_in_place(q, q_out, "q_out")) != EXL3_OK) return st;
+  if ((st = check_rows(k, "k", tokens, D, false)) != EXL3_OK) return st;
+  if (k_out != nullptr) {
+    if ((st = check_rows(k_out, "k_out", tokens, D, true)) != EXL3_OK) return st;
+    if ((st = check_in_place(k, k_out, "k_out")) != EXL3_OK) return st;
+  }
+  if ((st = check_rows(v, "v", tokens, D, false)) != EXL3_OK) return st;
+  if (k->heads != c->heads || v->heads != c->heads)
+    return host_fail(EXL3_ERR_INVALID_ARG, "k has %d heads, v %d, the cache %d", k->heads, v->heads, c->heads);
+  if ((st = check_norm(n, q, k)) != EXL3_OK) return st;
+  if ((st = check_launch_rows(tokens, q->heads + 2 * (int64_t)c->heads)) != EXL3_OK) return st;
+  if (tokens == 0) return EXL3_OK;
+  if ((st = check_ints(slots, "slots")) != EXL3_OK) return st;
+  NormRowsParams p = norm_rows(r, n, positions, axis_stride, tokens, D, q, q_out, k, k_out);
+  p.rows.v = rows_of(v);
+  p.rows.hv = c->heads;
+  p.rows.slots = slots;
+  p.rows.cache = view_of(c);
+  return launched(launch_norm_rows(D, c->dtype == EXL3_BF16, c->bits, p, (hipStream_t)stream),
+                  "norm, rope and cache write launch");
+}
+
+exl3_status exl3_cache_extend(int32_t pages, int32_t page_size, const int32_t *q_len, const int32_t *kv_len,
+                              int32_t batch, int32_t *page_table, int64_t page_table_stride, int32_t page_table_width,
+                              const int32_t *free_pages, int32_t n_free, const int32_t *taken, int32_t tokens,
+                              int32_t *cu_q, int32_t *kv_out, int32_t *positions, int32_t *slots, int32_t *counts,
+                              void *stream) {
+  host_clear_error();
+  exl3_status st;
+  if ((st = check_pages(pages, page_size)) != EXL3_OK) return st;
+  if (batch < 0 || batch > MAX_BATCH)
+    return host_fail(EXL3_ERR_INVALID_ARG, "batch=%d, must be 0..%d", batch, MAX_BATCH);
+  if (tokens < 0 || tokens > MAX_TOKENS)
+    return host_fail(EXL3_ERR_INVALID_ARG, "tokens=%d, must be 0..%d", tokens, MAX_TOKENS);
+  if (n_free < 0) return host_fail(EXL3_ERR_INVALID_ARG, "n_free=%d is negative", n_free);
+  if (page_table_width < 0 || (batch > 1 && page_table_stride < page_table_width))
+    return host_fail(EXL3_ERR_INVALID_ARG, "page table width=%d stride=%lld: rows of %d entries overlap",
+                     page_table_width, (long long)page_table_stride, page_table_width);
+  if (page_table_stride < 0 || page_table_stride > (1ll << 40))
+    return host_fail(EXL3_ERR_INVALID_ARG, "page table stride=%lld, must be 0..2^40", (long long)page_table_stride);
+  const int64_t entries = batch > 0 && page_table_width > 0 ? (int64_t)(batch - 1) * page_table_stride + page_table_width : 0;
+  struct Array {
+    const void *data;
+    int64_t n;
+    const char *name;
+    bool output;
+  };
+  const Array arrays[] = {{q_len, batch, "q_len", false},
+                          {kv_len, batch, "kv_len", false},
+                          {free_pages, n_free, "free_pages", false},
+                          {taken, taken != nullptr, "taken", false},
+                          {page_table, entries, "page_table", true},
+                          {cu_q, batch + 1, "cu_q", true},
+                          {kv_out, batch, "kv_out", true},
+                          {positions, tokens, "positions", true},
+                          {slots, tokens, "slots", true},
+                          {counts, 2, "counts", true}};
+  for (const Array &a : arrays)
+    if (a.n > 0 && (st = check_ints(a.data, a.name)) != EXL3_OK) return st;
+  for (const Array &a : arrays)
+    for (const Array &b : arrays)
+      if (&a < &b && (a.output || b.output) && overlap(a.data, a.n, b.data, b.n))
+        return host_fail(EXL3_ERR_INVALID_ARG, "%s and %s overlap", a.name, b.name);
+  TablesParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q_len = q_len;
+  p.kv_len = kv_len;
+  p.table = page_table;
+  p.table_stride = page_table_stride;
+  p.free_pages = free_pages;
+  p.taken = taken;
+  p.cu = cu_q;
+  p.kv_out = kv_out;
+  p.positions = positions;
+  p.slots = slots;
+  p.counts = counts;
+  p.batch = batch;
+  p.tokens = tokens;
+  p.width = page_table_width;
+  p.pages = pages;
+  p.page_shift = __builtin_ctz((unsigned)page_size);
+  p.n_free = n_free;
+  return launched(launch_tables(p, (hipStream_t)stream), "table launch");
+}
+
+}  // extern "C"
