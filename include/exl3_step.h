@@ -73,6 +73,21 @@ exl3_status exl3_cache_extend(int32_t pages, int32_t page_size, const int32_t *q
                               int32_t *cu_q, int32_t *kv_out, int32_t *positions, int32_t *slots, int32_t *counts,
                               void *stream);
 
+/* exl3_paged_attention and exl3_prompt_attention (causal) with a window of at
+ * least 1 and first tokens that stay visible: a row at position p sees the keys
+ * p-window+1..p and 0..sinks-1 (up to p), each once.  sinks is at most 2^20.
+ * Pages that hold neither may be holes at no cost.  Workspace:
+ * exl3_attention_workspace_bytes. */
+exl3_status exl3_paged_attention_sinks(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
+                                       const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
+                                       int64_t page_table_stride, int32_t page_table_width, int32_t batch,
+                                       int32_t tokens, float scale, int32_t window, int32_t sinks, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, const exl3_rows *v,
+                                        const exl3_rows *out, const int32_t *cu, int32_t batch, int32_t tokens,
+                                        int32_t head_dim, int32_t dtype, int32_t window, int32_t sinks, float scale,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -92,6 +92,8 @@ def _lib():
             "exl3_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
             "exl3_norm_rope": (i32, [A, N, vp, i64, i32, i32, i32, R, R, R, R, vp]),
             "exl3_norm_rope_cache_write": (i32, [C, A, N, vp, i64, vp, i32, R, R, R, R, R, vp]),
+            "exl3_paged_attention_sinks": (i32, [C, R, R, vp, vp, vp, i64, i32, i32, i32, f32, i32, i32, vp, sz, vp]),
+            "exl3_prompt_attention_sinks": (i32, [R, R, R, R, vp, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp]),
             "exl3_cache_extend": (i32, [i32, i32, vp, vp, i32, vp, i64, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
@@ -182,6 +184,13 @@ def _window(window: int) -> int:
     if not 0 <= window <= 1 << 30:
         raise ValueError(f"window={window}, must be 0 (none) to {1 << 30}")
     return window
+
+
+def _sinks(sinks: int, window: int) -> int:
+    """sinks for the library; 0 where nothing hides the first tokens anyway."""
+    if not 0 <= sinks <= 1 << 20:
+        raise ValueError(f"sinks={sinks}, must be 0 (none) to {1 << 20}")
+    return sinks if window > 0 else 0
 
 
 def _same_device(r: "Rope", q: torch.Tensor) -> None:
@@ -540,17 +549,17 @@ def attention_workspace_bytes(batch: int, tokens: int, q_heads: int, kv_heads: i
 
 def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor,
                     page_table: torch.Tensor, scale: Optional[float] = None, window: int = 0,
-                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    out: Optional[torch.Tensor] = None, sinks: int = 0) -> torch.Tensor:
     """Attention of new tokens over the cache, which already holds their own keys and values.
 
     q [tokens, q_heads, head_dim]: sequence s has rows cu_q[s]..cu_q[s+1]-1 (int32 [batch+1]) and kv_len[s] keys
     (int32 [batch]); its last row is at position kv_len[s]-1.  A row sees the keys up to its own position (window > 0:
-    the last `window` of them).  page_table int32 [batch, width]: the page of keys j*page_size...; pages that are not
+    the last `window` of them, and those of the sequence's first `sinks` tokens).  page_table int32 [batch, width]: the page of keys j*page_size...; pages that are not
     the cache's (-1) are holes.  scale defaults to head_dim^-0.5.  Rows that see no key are zero.
     out may be q (in place), and else overlaps neither it nor the cache."""
     if _current_device() != cache.device.index:
         with torch.cuda.device(cache.device):
-            return paged_attention(cache, q, cu_q, kv_len, page_table, scale, window, out)
+            return paged_attention(cache, q, cu_q, kv_len, page_table, scale, window, out, sinks)
     T, H, D = q.shape
     B = kv_len.shape[0]
     dev = cache.device
@@ -561,6 +570,12 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
     need = L.exl3_attention_workspace_bytes(B, T, H, cache.heads, D)
     stream = _raw_stream(dev.index)
     ws, wsn = _scratch(need, dev, stream)
+    if sinks and _sinks(sinks, window):
+        _check(L.exl3_paged_attention_sinks(cache._ref, ctypes.byref(qr), ctypes.byref(o), _ints(cu_q, "cu_q", B + 1, dev),
+                                            _ints(kv_len, "kv_len", B, dev), page_table.data_ptr(), page_table.stride(0),
+                                            page_table.shape[1], B, T, D ** -0.5 if scale is None else scale,
+                                            _window(window), sinks, ws, wsn, stream))
+        return out
     _check(L.exl3_paged_attention(cache._ref, ctypes.byref(qr), ctypes.byref(o), _ints(cu_q, "cu_q", B + 1, dev),
                                   _ints(kv_len, "kv_len", B, dev), page_table.data_ptr(), page_table.stride(0),
                                   page_table.shape[1], B, T, D ** -0.5 if scale is None else scale, _window(window), ws, wsn,
@@ -569,22 +584,29 @@ def paged_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len:
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, causal: bool = True,
-                     window: int = 0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     window: int = 0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     sinks: int = 0) -> torch.Tensor:
     """Attention within packed sequences: q [tokens, q_heads, head_dim], k and v [tokens, kv_heads, head_dim], sequence
     s the rows cu_seqlens[s]..cu_seqlens[s+1]-1 (int32 [batch+1]).  causal: a row sees the rows of its sequence up to
-    itself (window > 0: the last `window` of them), else all.  scale defaults to head_dim^-0.5.  out may be q (in place),
+    itself (window > 0: the last `window` of them, and the sequence's first `sinks` rows), else all.  scale defaults to head_dim^-0.5.  out may be q (in place),
     and else overlaps none of q, k and v."""
     T, H, D = q.shape
     B = cu_seqlens.shape[0] - 1
     qr, kr, vr = _rows(q, "q"), _rows(k, "k", q), _rows(v, "v", q)
     if _current_device() != q.device.index:
         with torch.cuda.device(q.device):
-            return prompt_attention(q, k, v, cu_seqlens, causal, window, scale, out)
+            return prompt_attention(q, k, v, cu_seqlens, causal, window, scale, out, sinks)
     out, o = _out(out, q, "out")
     L = _lib()
     need = L.exl3_attention_workspace_bytes(B, T, H, k.shape[1], D)
     stream = _raw_stream(q.device.index)
     ws, wsn = _scratch(need, q.device, stream)
+    if sinks and _sinks(sinks, window) and causal:
+        _check(L.exl3_prompt_attention_sinks(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(o),
+                                             _ints(cu_seqlens, "cu_seqlens", B + 1, q.device), B, T, D,
+                                             _dtype_id(q.dtype, "q"), _window(window), sinks,
+                                             D ** -0.5 if scale is None else scale, ws, wsn, stream))
+        return out
     _check(L.exl3_prompt_attention(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(o),
                                    _ints(cu_seqlens, "cu_seqlens", B + 1, q.device), B, T, D, _dtype_id(q.dtype, "q"),
                                    int(causal), _window(window), D ** -0.5 if scale is None else scale, ws, wsn, stream))

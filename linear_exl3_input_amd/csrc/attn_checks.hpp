@@ -256,4 +256,116 @@ inline exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads
   return EXL3_OK;
 }
 
+// The checks of a call over the cache, and its parameters but for what run_attention
+// adds.  Without tokens p.tokens is 0 and the rest of p unset.
+inline exl3_status paged_params(AttnParams &p, const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
+                                const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
+                                int64_t page_table_stride, int32_t page_table_width, int32_t batch, int32_t tokens,
+                                float scale, int32_t window) {
+  exl3_status st;
+  if ((st = check_cache(c)) != EXL3_OK) return st;
+  const int32_t D = c->head_dim;
+  if ((st = check_shape(tokens, D, c->dtype)) != EXL3_OK) return st;
+  if ((st = check_rows(q, "q", tokens, D, false)) != EXL3_OK) return st;
+  if ((st = check_rows(out, "out", tokens, D, true)) != EXL3_OK) return st;
+  if (q->heads != out->heads)
+    return host_fail(EXL3_ERR_INVALID_ARG, "out has %d heads, q %d", out->heads, q->heads);
+  if ((st = check_attention_sizes(batch, tokens, q->heads, c->heads)) != EXL3_OK) return st;
+  if (page_table_width < 0 || page_table_stride < 0)
+    return host_fail(EXL3_ERR_INVALID_ARG, "page table width=%d stride=%lld are negative", page_table_width,
+                     (long long)page_table_stride);
+  if (window < 0 || window > MAX_WINDOW)
+    return host_fail(EXL3_ERR_INVALID_ARG, "window=%d, must be 0 (none) to %d", window, MAX_WINDOW);
+  if ((st = check_scale(scale)) != EXL3_OK) return st;
+  std::memset(&p, 0, sizeof p);
+  if (tokens == 0) return EXL3_OK;
+  if (batch == 0) return host_fail(EXL3_ERR_INVALID_ARG, "batch=0 with %d tokens", tokens);
+  if ((st = check_ints(cu_q, "cu_q")) != EXL3_OK) return st;
+  if ((st = check_ints(kv_len, "kv_len")) != EXL3_OK) return st;
+  if (page_table_width > 0 && (st = check_ints(page_table, "page_table")) != EXL3_OK) return st;
+  p.q = rows_of(q);
+  p.out = rows_of(out);
+  p.cache = view_of(c);
+  p.cu = cu_q;
+  p.kv_len = kv_len;
+  p.page_table = page_table;
+  p.table_stride = page_table_stride;
+  p.table_width = page_table_width;
+  p.table_keys = (int32_t)std::min<int64_t>((int64_t)page_table_width * c->page_size, MAX_KEYS);
+  p.batch = batch;
+  p.tokens = tokens;
+  p.heads_kv = c->heads;
+  p.group = q->heads / c->heads;
+  p.by_group = Divisor::of((uint32_t)p.group);
+  p.causal = 1;
+  p.window = window;
+  p.scale_log2 = scale * LOG2E;
+  return EXL3_OK;
+}
+
+// The same for a call over packed rows.
+inline exl3_status prompt_params(AttnParams &p, const exl3_rows *q, const exl3_rows *k, const exl3_rows *v,
+                                 const exl3_rows *out, const int32_t *cu, int32_t batch, int32_t tokens,
+                                 int32_t head_dim, int32_t dtype, int32_t causal, int32_t window, float scale) {
+  exl3_status st;
+  if ((st = check_shape(tokens, head_dim, dtype)) != EXL3_OK) return st;
+  if ((st = check_rows(q, "q", tokens, head_dim, false)) != EXL3_OK) return st;
+  if ((st = check_rows(k, "k", tokens, head_dim, false)) != EXL3_OK) return st;
+  if ((st = check_rows(v, "v", tokens, head_dim, false)) != EXL3_OK) return st;
+  if ((st = check_rows(out, "out", tokens, head_dim, true)) != EXL3_OK) return st;
+  if (q->heads != out->heads)
+    return host_fail(EXL3_ERR_INVALID_ARG, "out has %d heads, q %d", out->heads, q->heads);
+  // tiles of up to 128 keys are addressed with 32-bit offsets
+  constexpr int64_t MAX_TOKEN_STRIDE = 1 << 22;
+  if (k->token_stride > MAX_TOKEN_STRIDE || v->token_stride > MAX_TOKEN_STRIDE)
+    return host_fail(EXL3_ERR_UNSUPPORTED, "token strides of k (%lld) and v (%lld) must be at most %lld elements",
+                     (long long)k->token_stride, (long long)v->token_stride, (long long)MAX_TOKEN_STRIDE);
+  if (k->heads != v->heads) return host_fail(EXL3_ERR_INVALID_ARG, "k has %d heads, v %d", k->heads, v->heads);
+  if ((st = check_attention_sizes(batch, tokens, q->heads, k->heads)) != EXL3_OK) return st;
+  if (causal != 0 && causal != 1) return host_fail(EXL3_ERR_INVALID_ARG, "causal=%d, must be 0 or 1", causal);
+  if (window < 0 || window > MAX_WINDOW || (window > 0 && !causal))
+    return host_fail(EXL3_ERR_INVALID_ARG, "window=%d with causal=%d: 0 (none) to %d, and a window is causal", window,
+                     causal, MAX_WINDOW);
+  if ((st = check_scale(scale)) != EXL3_OK) return st;
+  std::memset(&p, 0, sizeof p);
+  if (tokens == 0) return EXL3_OK;
+  if (batch == 0) return host_fail(EXL3_ERR_INVALID_ARG, "batch=0 with %d tokens", tokens);
+  if ((st = check_ints(cu, "cu")) != EXL3_OK) return st;
+  p.q = rows_of(q);
+  p.out = rows_of(out);
+  p.k = rows_of(k);
+  p.v = rows_of(v);
+  p.cu = cu;
+  p.batch = batch;
+  p.tokens = tokens;
+  p.heads_kv = k->heads;
+  p.group = q->heads / k->heads;
+  p.by_group = Divisor::of((uint32_t)p.group);
+  p.causal = causal;
+  p.window = window;
+  p.scale_log2 = scale * LOG2E;
+  return EXL3_OK;
+}
+
+// Launches by launch(columns), the tile kernel's columns being 0.
+template <class Launch>
+exl3_status run_attention(AttnParams &p, int32_t head_dim, int32_t q_heads, void *workspace, size_t workspace_bytes,
+                          Launch launch) {
+  AttnPlan pl;
+  exl3_status st = plan_attention(p.batch, p.tokens, q_heads, p.heads_kv, head_dim, &pl);
+  if (st != EXL3_OK) return st;
+  if (pl.workspace > 0) {
+    if (workspace == nullptr || workspace_bytes < pl.workspace)
+      return host_fail(EXL3_ERR_WORKSPACE, "workspace of %zu bytes; this call needs %zu (short by %zu)", workspace_bytes,
+                       pl.workspace, pl.workspace > workspace_bytes ? pl.workspace - workspace_bytes : (size_t)0);
+    if ((st = check_ptr(workspace, "workspace")) != EXL3_OK) return st;
+    p.counters = static_cast<uint32_t *>(workspace);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + EXL3_WORKSPACE_COUNTER_BYTES);
+  }
+  p.target = pl.target;
+  p.part_min = pl.part_min;
+  p.part_cap = pl.part_cap;
+  return launched(launch(pl.columns), "attention launch");
+}
+
 }  // namespace exl3

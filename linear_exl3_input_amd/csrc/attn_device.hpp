@@ -170,7 +170,7 @@ struct Work {
 // `target`, so that they end up near it (whole rounds of the GPU) but for
 // lengths that rounding up hits hard; it is at least part_min.  There are
 // never more than tiles + target items, nor 2 * target parts.
-template <int R>
+template <int R, int KIND = ATTN_PLAIN>
 __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w) {
   struct Seq {
     int q0, ql, kv, tiles, span;
@@ -195,7 +195,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
     x.tiles = (int)(((int64_t)x.ql * p.group + R - 1) / R);
     // a tile's rows are at most R tokens; its keys start at a multiple of 32
     x.span = p.kv_len ? min(x.kv, p.table_keys) : x.kv;
-    if (p.window > 0) x.span = min(x.span, p.window + R + 32);
+    if (p.window > 0) x.span = min(x.span, p.window + R + 32 + (KIND == ATTN_SINKS ? p.sink_keys : 0));
     return x;
   };
   int head_end = 0, from;
@@ -264,6 +264,8 @@ struct KeyRange {
   int shift;            // a new token's position is its index + shift
   int p_first, p_last;  // positions of the first and the last row
   int start, lo, hi;
+  int end;              // where the workgroup's steps end: hi, but see sink_range
+  int sinks, sink_end, skip;
 };
 
 __device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w, int r0, int r_last) {
@@ -280,6 +282,34 @@ __device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w
     k.hi = (int)min<int64_t>(from + w.part_keys, k.hi);
   }
   k.start = k.lo & ~31;
+  k.end = k.hi;
+  return k;
+}
+
+// The same for rows that see a window, lo .. of the first row to hi, and the
+// first `sinks` keys.  Steps of whole tiles of G keys go over places: the first
+// keys' tiles, then from the multiple of 32 at or below lo on; place x from
+// sink_end on is key x + skip.  (Where those tiles reach the window, every place
+// is its key.)  Parts are ranges of places; lo and hi stay those of the tile.
+template <int G>
+__device__ __forceinline__ KeyRange sink_range(const AttnParams &p, const Work &w, int r0, int r_last) {
+  KeyRange k;
+  k.shift = w.kv_len - w.q_len;
+  k.p_first = k.shift + quotient(r0, p.by_group);
+  k.p_last = k.shift + quotient(r_last, p.by_group);
+  k.hi = min(w.kv_len, k.p_last + 1);
+  if (p.kv_len) k.hi = min(k.hi, p.table_keys);
+  k.lo = max(0, k.p_first - p.window + 1);
+  k.sinks = min(p.sinks, k.hi);
+  k.sink_end = (max(k.sinks, 0) + G - 1) & ~(G - 1);
+  k.skip = max(0, (k.lo & ~31) - k.sink_end);
+  k.end = max(k.hi - k.skip, min(k.hi, k.sink_end));  // (the table may end before the window)
+  k.start = 0;
+  if (w.splits > 1) {
+    const int64_t from = (int64_t)w.split * w.part_keys;
+    k.start = (int)min<int64_t>(from, MAX_KEYS);
+    k.end = (int)min<int64_t>(from + w.part_keys, k.end);
+  }
   return k;
 }
 

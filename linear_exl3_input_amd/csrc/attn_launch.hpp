@@ -99,6 +99,13 @@ struct AttnParams {
   int32_t target;             // work items per head aimed at when keys are split (0: not split)
   int32_t part_min;           // least keys of a part
   int32_t part_cap;           // parts of a head that `part` and `counters` hold
+  int32_t sinks, sink_keys;   // ATTN_SINKS: first keys that stay visible, and that rounded up to whole tiles
+};
+
+// What a kernel computes, apart from the head size, the types and the tiles.
+enum AttnKind {
+  ATTN_PLAIN = 0,  // a range of keys for each row
+  ATTN_SINKS = 1,  // a causal window, and the first keys
 };
 
 // bits: 0 (no cache), 16, 8, 4.
@@ -112,5 +119,7 @@ hipError_t launch_attn_small(int head_dim, bool bf16, int bits, const AttnParams
 // Tiles of ATTN_TILE_ROWS query rows.
 constexpr int ATTN_TILE_ROWS = 128;
 hipError_t launch_attn_tile(int head_dim, bool bf16, int bits, const AttnParams &p, hipStream_t s);
+// ATTN_SINKS; columns as above, 0: tiles of ATTN_TILE_ROWS.
+hipError_t launch_attn_sinks(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
 
 }  // namespace exl3

@@ -148,9 +148,9 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Work &w, in
   }
 }
 
-template <bool BF16, int D, int BITS, int NT>
+template <bool BF16, int D, int BITS, int NT, int KIND = ATTN_PLAIN>
 __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(AttnParams p) {
-  constexpr bool PAGED = BITS != 0;
+  constexpr bool PAGED = BITS != 0, SINKS = KIND == ATTN_SINKS;
   constexpr int CB = PAGED ? BITS : 16;  // bits of a stored value
   constexpr int R = 16 * NT;
   constexpr int DV = D / 16;             // dims of a row that a lane holds of the second product
@@ -165,14 +165,21 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   const int head = workgroup() % p.heads_kv;
   const int item = workgroup() / p.heads_kv;
   Work w;
-  if (!find_work<R>(p, item, lane, w)) return;
+  if (!find_work<R, KIND>(p, item, lane, w)) return;
 
   // ---- the tile's rows and their keys
   const int rows = w.q_len * p.group;
   const int r0 = w.tile * R;
   const int r_last = min(r0 + R, rows) - 1;
-  const KeyRange kr = key_range(p, w, r0, r_last);
+  const KeyRange kr = SINKS ? sink_range<32>(p, w, r0, r_last) : key_range(p, w, r0, r_last);
   const int lo = kr.lo, hi = kr.hi, p_first = kr.p_first, p_last = kr.p_last, shift = kr.shift;
+  const int end = SINKS ? kr.end : hi;
+  // the key at place x of the steps
+  auto key_at = [&](int x) __attribute__((always_inline)) { return SINKS && x >= kr.sink_end ? x + kr.skip : x; };
+  // whether some row sees key k, holes aside
+  auto useful = [&](int k) __attribute__((always_inline)) {
+    return (uint32_t)(k - lo) < (uint32_t)(SINKS ? max(0, hi - lo) : hi - lo) || (SINKS && k < kr.sinks);
+  };
 
   // ---- where keys and values lie
   const int ps_mask = (1 << p.cache.page_shift) - 1;
@@ -190,12 +197,13 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   int k0 = kr.start + 32 * wave;
   int pk = 0, pv = 0, pk2 = 0, pv2 = 0;  // pages of this step's and the next step's keys and values
   if constexpr (PAGED) {
-    pk = page_of(k0 + 8 * (c >> 2));
-    pv = page_of(k0 + 8 * g);
-    pk2 = page_of(k0 + 128 + 8 * (c >> 2));
-    pv2 = page_of(k0 + 128 + 8 * g);
+    pk = page_of(key_at(k0) + 8 * (c >> 2));
+    pv = page_of(key_at(k0) + 8 * g);
+    pk2 = page_of(key_at(k0 + 128) + 8 * (c >> 2));
+    pv2 = page_of(key_at(k0 + 128) + 8 * g);
   }
   int first[NT], span[NT];  // the keys first .. first + span - 1 are those the lane's row (column c of tile n) sees
+  int sink[NT];             // and, with SINKS, 0 .. sink - 1
   const uint16_t *q_row[NT];
   bool live[NT];
 #pragma unroll
@@ -207,6 +215,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     const int pos = shift + i;
     first[n] = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
     span[n] = max(0, (p.causal ? min(hi, pos + 1) : hi) - first[n]);
+    sink[n] = SINKS ? min(kr.sinks, pos + 1) : 0;
     q_row[n] = p.q.data + (int64_t)(w.q0 + i) * p.q.token + (int64_t)(head * p.group + h) * p.q.head;
   }
   // B operands of the first product: dims in the order the key loads have
@@ -221,8 +230,8 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 
   uint32_t kw[2][KR::LOADS][KR::WORDS], vw[8][VW];
   uint32_t ksc[2][2], vsc[8];  // scale bytes: of a key's row, of the lane's block of a value row
-  auto load_k = [&](int k0, int pg) __attribute__((always_inline)) {
-    const int key = k0 + 8 * (c >> 2) + (c & 3);
+  auto load_k = [&](int at, int pg) __attribute__((always_inline)) {
+    const int key = key_at(at) + 8 * (c >> 2) + (c & 3);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const uint8_t *a;
@@ -248,10 +257,11 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
       }
     }
   };
-  auto load_v = [&](int k0, int pg) __attribute__((always_inline)) {
+  auto load_v = [&](int at, int pg) __attribute__((always_inline)) {
+    const int key0 = key_at(at);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int key = k0 + 8 * g + i;
+      const int key = key0 + 8 * g + i;
       const uint8_t *a;
       if constexpr (PAGED) {
         const int64_t r = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
@@ -269,6 +279,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 
   // whether every row sees every key of the step at k (holes aside)
   auto whole_step = [&](int k) __attribute__((always_inline)) {
+    if (SINKS && k + 32 <= min(kr.sinks, p_first + 1)) return true;
     return k >= lo && k + 32 <= hi && (!p.causal || k + 31 <= p_first) && (p.window == 0 || k > p_last - p.window);
   };
 
@@ -282,17 +293,18 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     for (int j = 0; j < DV; ++j) o[n][j] = (float4_t){0.f, 0.f, 0.f, 0.f};
   }
 
-  if (k0 < hi) {
+  if (k0 < end) {
     load_k(k0, pk);
     load_v(k0, pv);
   }
   bool odd = false;  // some value that not all rows see is an infinity or NaN
-  for (; k0 < hi; k0 += 128) {
-    const bool more = k0 + 128 < hi;
+  for (; k0 < end; k0 += 128) {
+    const bool more = k0 + 128 < end;
+    const int key0 = key_at(k0);
     int pk3 = 0, pv3 = 0;
     if constexpr (PAGED) {
-      pk3 = page_of(k0 + 256 + 8 * (c >> 2));
-      pv3 = page_of(k0 + 256 + 8 * g);
+      pk3 = page_of(key_at(k0 + 256) + 8 * (c >> 2));
+      pv3 = page_of(key_at(k0 + 256) + 8 * g);
     }
     // ---- scores
     float4_t s[NT][2];
@@ -315,9 +327,9 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
       }
     }
     if (more) load_k(k0 + 128, pk2);
-    // ---- mask: key of score (t, i) is k0 + 8g + 4t + i
+    // ---- mask: key of score (t, i) is key0 + 8g + 4t + i
     const bool hole = PAGED && pv < 0;
-    const bool whole = whole_step(k0) && !__any(hole);
+    const bool whole = whole_step(key0) && !__any(hole);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -329,7 +341,9 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const bool ok = (uint32_t)(k0 + 8 * g + 4 * t + i - first[n]) < (hole ? 0u : (uint32_t)span[n]);
+            const int key = key0 + 8 * g + 4 * t + i;
+            bool ok = (uint32_t)(key - first[n]) < (hole ? 0u : (uint32_t)span[n]);
+            if (SINKS) ok = ok || key < (hole ? 0 : sink[n]);
             s[n][t][i] = ok ? s[n][t][i] : -INFINITY;
           }
       }
@@ -370,7 +384,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     if (!whole) {  // keys outside the range or in a hole: whatever is stored there counts as zero
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if ((uint32_t)(k0 + 8 * g + i - lo) >= (hole ? 0u : (uint32_t)(hi - lo))) {
+        if (hole || !useful(key0 + 8 * g + i)) {
 #pragma unroll
           for (int x = 0; x < VW; ++x) vw[i][x] = 0u;
           if constexpr (CB < 16) vsc[i] = 127u;
@@ -413,11 +427,12 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   if (__any(odd)) {
     // rare: once more over the wave's steps that not all rows see whole
 #pragma unroll 1
-    for (int k = kr.start + 32 * wave; k < hi; k += 128) {
+    for (int at = kr.start + 32 * wave; at < end; at += 128) {
+      const int k = key_at(at);
 #pragma unroll 1
-      for (int key = max(k, lo); key < min(k + 32, hi); ++key) {
+      for (int key = SINKS ? k : max(k, lo); key < min(k + 32, hi); ++key) {
         const int pg = PAGED ? page_of(key) : 0;
-        if (pg < 0 || (whole_step(k) && !__any(PAGED && page_of(k + 8 * g) < 0))) continue;
+        if (pg < 0 || (SINKS && !useful(key)) || (whole_step(k) && !__any(PAGED && page_of(k + 8 * g) < 0))) continue;
         const int64_t row = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -441,7 +456,10 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
               const float f = Half<BF16>::up(j ? u >> 16 : u & 0xFFFFu);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                o[n][2 * x + j][i] += (uint32_t)(key - first[n]) < (uint32_t)span[n] && !__builtin_isfinite(f) ? f : 0.f;
+                o[n][2 * x + j][i] += ((uint32_t)(key - first[n]) < (uint32_t)span[n] || (SINKS && key < sink[n])) &&
+                                              !__builtin_isfinite(f)
+                                          ? f
+                                          : 0.f;
             }
           }
         }

@@ -88,10 +88,10 @@ struct TileGeom {
   static constexpr int BUF = K_BYTES + V_BYTES;
 };
 
-template <bool BF16, int D, int BITS>
+template <bool BF16, int D, int BITS, int KIND = ATTN_PLAIN>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnParams p) {
   using G = TileGeom<D>;
-  constexpr bool PAGED = BITS != 0;
+  constexpr bool PAGED = BITS != 0, SINKS = KIND == ATTN_SINKS;
   constexpr int CB = PAGED ? BITS : 16;
   constexpr int R = ATTN_TILE_ROWS, BN = G::BN, NS = G::NS, NC = G::NC, DT = G::DT;
   constexpr int PW = CB / 4;  // words of 8 values: 4, 2 or 1
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int head = workgroup() % p.heads_kv;
   const int item = workgroup() / p.heads_kv;
   Work w;
-  if (!find_work<R>(p, item, lane, w)) return;
+  if (!find_work<R, KIND>(p, item, lane, w)) return;
   const int rows = w.q_len * p.group;
   {
     // a sequence's last tiles have the most keys and go first
@@ -115,20 +115,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // ---- the tile's rows and their keys
   const int r0 = w.tile * R;
   const int r_last = min(r0 + R, rows) - 1;
-  const KeyRange kr = key_range(p, w, r0, r_last);
+  const KeyRange kr = SINKS ? sink_range<BN>(p, w, r0, r_last) : key_range(p, w, r0, r_last);
   const int lo = kr.lo, hi = kr.hi, p_first = kr.p_first, p_last = kr.p_last, shift = kr.shift;
   const int start = kr.start;
-  const int n_tiles = hi > lo ? (hi - start + BN - 1) / BN : 0;
+  const int n_tiles = SINKS ? max(0, kr.end - start + BN - 1) / BN : hi > lo ? (hi - start + BN - 1) / BN : 0;
+  // the first key of tile t
+  auto tile_key = [&](int t) __attribute__((always_inline)) {
+    const int x = start + t * BN;
+    return SINKS && x >= kr.sink_end ? x + kr.skip : x;
+  };
+  // whether some row sees key k, holes aside
+  auto useful = [&](int k) __attribute__((always_inline)) {
+    return (uint32_t)(k - lo) < (uint32_t)(SINKS ? max(0, hi - lo) : hi - lo) || (SINKS && k < kr.sinks);
+  };
 
   // ---- the lane's row, which sees the keys first .. first + span - 1
   const int row = r0 + 32 * wave + col;
   const int pos = shift + quotient(min(row, r_last), p.by_group);
   const int first = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
   const int span = max(0, (p.causal ? min(hi, pos + 1) : hi) - first);
+  const int sink = SINKS ? min(kr.sinks, pos + 1) : 0;  // and, with SINKS, 0 .. sink - 1
   // of the wave's rows, first to last, every one sees [w_lo, w_hi)
   const int wp0 = shift + quotient(min(r0 + 32 * wave, r_last), p.by_group);
   const int wp1 = shift + quotient(min(r0 + 32 * wave + 31, r_last), p.by_group);
   const int w_hi = p.causal ? min(hi, wp0 + 1) : hi, w_lo = p.window > 0 ? max(lo, wp1 - p.window + 1) : lo;
+  const int w_sink = SINKS ? min(kr.sinks, wp0 + 1) : 0;
   // Whole rows pass between memory and the wave's registers through its quarter
   // of LDS (before the first and after the last tile): a row's D / 8 pieces by
   // as many lanes side by side, where the lane's own 16 bytes of 32 rows each
@@ -178,8 +189,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // read as zeros (and nothing is read past the last tile).  The check sees the
   // vector offset alone, so a row's place is there and not in the scalar one.
   auto packed = [&](const Rows &x, int t) __attribute__((always_inline)) {
-    const int n = min(hi - start - t * BN, BN);  // the host keeps a tile's rows within 2^31 bytes
-    return __builtin_amdgcn_make_buffer_rsrc(x.data + head * x.head + (int64_t)(w.q0 + start + t * BN) * x.token, (short)0,
+    const int n = min(hi - tile_key(t), BN);  // the host keeps a tile's rows within 2^31 bytes
+    return __builtin_amdgcn_make_buffer_rsrc(x.data + head * x.head + (int64_t)(w.q0 + tile_key(t)) * x.token, (short)0,
                                              n > 0 ? (n - 1) * ((int)x.token * 2) + D * 2 : 0, 0x00020000);
   };
   // The loads of keys tk and values tv, in 12 pieces (4 of keys, 8 of values)
@@ -187,8 +198,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // masked and its values zeroed.
   auto fetch = [&](int tk, int kpg, int tv, int vpg) __attribute__((always_inline)) {
     if constexpr (PAGED) {
-      const int64_t kat = ((int64_t)head << p.cache.page_shift) + ((start + tk * BN + ka) & ps_mask);
-      const int64_t vat = ((int64_t)head << p.cache.page_shift) + ((start + tv * BN + va) & ps_mask);
+      const int64_t kat = ((int64_t)head << p.cache.page_shift) + ((tile_key(tk) + ka) & ps_mask);
+      const int64_t vat = ((int64_t)head << p.cache.page_shift) + ((tile_key(tv) + va) & ps_mask);
       const uint8_t *k = p.cache.k + max(kpg, 0) * p.cache.k_page + kat * ROW + c * CB;
       const uint8_t *v = p.cache.v + max(vpg, 0) * p.cache.v_page + vat * ROW + c * CB + half * (CB / 2);
       const uint8_t *ks = nullptr, *vs = nullptr;
@@ -230,7 +241,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // The first loads, and while they are on their way a look at every page for
   // holes and the wait for q (which inside the loop would also be one for the
   // tiles on their way).
-  auto key_page = [&](int t, int a) __attribute__((always_inline)) { return PAGED ? page_of(start + t * BN + a) : 0; };
+  auto key_page = [&](int t, int a) __attribute__((always_inline)) { return PAGED ? page_of(tile_key(t) + a) : 0; };
   int vpg = key_page(0, va);  // of the values in vraw
   int kpg_next = key_page(0, ka), vpg_next = key_page(1, va);
   u32x4_t q[D / 16];
@@ -254,8 +265,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   bool holes = false;
   if constexpr (PAGED) {
     int any = 0;
-    for (int i = (start >> p.cache.page_shift) + tid; ((int64_t)i << p.cache.page_shift) < hi; i += 256)
-      any |= page_of(max(i << p.cache.page_shift, start)) < 0;
+    if constexpr (SINKS) {  // 16 keys, which have one page, at a time: pages that no row sees may be gone
+      for (int at = 16 * tid; at < n_tiles * BN; at += 16 * 256) {
+        const int x = start + at, k = x >= kr.sink_end ? x + kr.skip : x;
+        any |= (k < kr.sinks || (k + 15 >= lo && k < hi)) && page_of(k) < 0;
+      }
+    } else {
+      for (int i = (start >> p.cache.page_shift) + tid; ((int64_t)i << p.cache.page_shift) < hi; i += 256)
+        any |= page_of(max(i << p.cache.page_shift, start)) < 0;
+    }
     holes = __syncthreads_or(any) != 0;
   } else {
     __syncthreads();
@@ -264,7 +282,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(q[s]));
   // whether every row of the workgroup sees every key of tile t
   auto whole_tile = [&](int t) __attribute__((always_inline)) {
-    const int k0 = start + t * BN;
+    const int k0 = tile_key(t);
+    if (SINKS && k0 + BN <= min(kr.sinks, p_first + 1)) return !holes;
     return k0 >= lo && k0 + BN <= hi && (!p.causal || k0 + BN - 1 <= p_first) &&
            (p.window == 0 || k0 > p_last - p.window) && !holes;
   };
@@ -283,7 +302,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bool in = (uint32_t)(start + t * BN + va + i - lo) < (uint32_t)(hi - lo) && (!PAGED || pg >= 0);
+      const bool in = useful(tile_key(t) + va + i) && (!PAGED || pg >= 0);
 #pragma unroll
       for (int y = 0; y < HW; ++y) {
         vraw[i][y] = in ? vraw[i][y] : 0u;
@@ -376,18 +395,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // The mask, and the running maximum.  True when it moved: o then has to be
   // multiplied by `keep`.
   auto settle = [&](int t, float &keep) __attribute__((always_inline)) -> bool {
-    const int k0 = start + t * BN;
-    if (!(k0 >= w_lo && k0 + BN <= w_hi && !holes)) {
+    const int k0 = tile_key(t);
+    if (!(((k0 >= w_lo && k0 + BN <= w_hi) || (SINKS && k0 + BN <= w_sink)) && !holes)) {
       // element 8t8 + i of product n is key k0 + 32n + 16t8 + 8h + i
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int t8 = 0; t8 < 2; ++t8) {
           const int key = k0 + 32 * n + 16 * t8 + 8 * h;
-          const uint32_t seen = PAGED && holes && page_of(key) < 0 ? 0u : (uint32_t)span;
+          const bool hole = PAGED && holes && page_of(key) < 0;
+          const uint32_t seen = hole ? 0u : (uint32_t)span;
+          const int seen_first = SINKS && !hole ? sink : 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            s[n][8 * t8 + i] = (uint32_t)(key + i - first) < seen ? s[n][8 * t8 + i] : -INFINITY;
+            s[n][8 * t8 + i] = (uint32_t)(key + i - first) < seen || (SINKS && key + i < seen_first) ? s[n][8 * t8 + i] : -INFINITY;
         }
     }
     float top = s[0][0];
@@ -532,11 +553,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
 #pragma unroll 1
     for (int t = 0; t < n_tiles; ++t) {
       if (whole_tile(t)) continue;
-      const int k0 = start + t * BN;
+      const int k0 = tile_key(t);
 #pragma unroll 1
-      for (int key = max(k0, lo); key < min(k0 + BN, hi); ++key) {
+      for (int key = SINKS ? k0 : max(k0, lo); key < min(k0 + BN, hi); ++key) {
         const int pg = PAGED ? page_of(key) : 0;
-        if (pg < 0) continue;
+        if (pg < 0 || (SINKS && !useful(key))) continue;
         const int64_t slot = ((int64_t)head << p.cache.page_shift) + (key & ps_mask);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
@@ -553,7 +574,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float f = Half<BF16>::up((v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
-            o[prod(j)][elem(x, j)] += (uint32_t)(key - first) < (uint32_t)span && !__builtin_isfinite(f) ? f : 0.f;
+            o[prod(j)][elem(x, j)] +=
+                ((uint32_t)(key - first) < (uint32_t)span || (SINKS && key < sink)) && !__builtin_isfinite(f) ? f : 0.f;
           }
         }
       }

@@ -76,7 +76,39 @@ bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {  // ranges 
   return an > 0 && bn > 0 && a != nullptr && b != nullptr && x < y + 4 * (uintptr_t)bn && y < x + 4 * (uintptr_t)an;
 }
 
+// Positions, sinks and windows stay within 32 bits.
+constexpr int32_t MAX_SINKS = 1 << 20;
+
+exl3_status check_sinks(int32_t sinks, int32_t window) {
+  if (sinks < 0 || sinks > MAX_SINKS)
+    return host_fail(EXL3_ERR_INVALID_ARG, "sinks=%d, must be 0..%d", sinks, MAX_SINKS);
+  if (window < 1) return host_fail(EXL3_ERR_INVALID_ARG, "window=%d: first tokens beside a window need one", window);
+  return EXL3_OK;
+}
+
+exl3_status run_sinks(AttnParams &p, int32_t head_dim, bool bf16, int32_t bits, int32_t q_heads, int32_t sinks,
+                      void *workspace, size_t workspace_bytes, hipStream_t s) {
+  p.sinks = sinks;
+  p.sink_keys = (sinks + 127) & ~127;  // both kernels' steps are at most 128 keys
+  return run_attention(p, head_dim, q_heads, workspace, workspace_bytes,
+                       [&](int columns) { return launch_attn_sinks(head_dim, bf16, bits, p, columns, s); });
+}
+
 }  // namespace
+
+namespace exl3 {
+
+hipError_t launch_attn_sinks_d64(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_sinks_d128(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_sinks_d256(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+
+hipError_t launch_attn_sinks(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s) {
+  return head_dim == 64    ? launch_attn_sinks_d64(bf16, bits, p, columns, s)
+         : head_dim == 128 ? launch_attn_sinks_d128(bf16, bits, p, columns, s)
+                           : launch_attn_sinks_d256(bf16, bits, p, columns, s);
+}
+
+}  // namespace exl3
 
 extern "C" {
 
@@ -199,6 +231,36 @@ exl3_status exl3_cache_extend(int32_t pages, int32_t page_size, const int32_t *q
   p.page_shift = __builtin_ctz((unsigned)page_size);
   p.n_free = n_free;
   return launched(launch_tables(p, (hipStream_t)stream), "table launch");
+}
+
+exl3_status exl3_paged_attention_sinks(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
+                                       const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
+                                       int64_t page_table_stride, int32_t page_table_width, int32_t batch,
+                                       int32_t tokens, float scale, int32_t window, int32_t sinks, void *workspace,
+                                       size_t workspace_bytes, void *stream) {
+  host_clear_error();
+  AttnParams p;
+  exl3_status st;
+  if ((st = check_sinks(sinks, window)) != EXL3_OK) return st;
+  st = paged_params(p, c, q, out, cu_q, kv_len, page_table, page_table_stride, page_table_width, batch, tokens, scale,
+                    window);
+  if (st != EXL3_OK || tokens == 0) return st;
+  return run_sinks(p, c->head_dim, c->dtype == EXL3_BF16, c->bits, q->heads, sinks, workspace, workspace_bytes,
+                   (hipStream_t)stream);
+}
+
+exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, const exl3_rows *v,
+                                        const exl3_rows *out, const int32_t *cu, int32_t batch, int32_t tokens,
+                                        int32_t head_dim, int32_t dtype, int32_t window, int32_t sinks, float scale,
+                                        void *workspace, size_t workspace_bytes, void *stream) {
+  host_clear_error();
+  AttnParams p;
+  exl3_status st;
+  if ((st = check_sinks(sinks, window)) != EXL3_OK) return st;
+  st = prompt_params(p, q, k, v, out, cu, batch, tokens, head_dim, dtype, 1, window, scale);
+  if (st != EXL3_OK || tokens == 0) return st;
+  return run_sinks(p, head_dim, dtype == EXL3_BF16, 0, q->heads, sinks, workspace, workspace_bytes,
+                   (hipStream_t)stream);
 }
 
 }  // extern "C"

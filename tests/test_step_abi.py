@@ -181,3 +181,34 @@ def test_reference_tables_by_hand():
     assert got[2] == [14, 15, 16, *range(20), 0, 0, 0]
     assert got[3] == [4 * 16 + 14, 4 * 16 + 15, 7 * 16, *range(128, 144), *range(144, 148), -1, -1, -1]
     assert got[5] == [[4, 7], [5, -1], [8, 9]]
+
+
+# ------------------------------------------------- windows with first tokens
+
+def paged_sinks(window=5, sinks=4, tokens=3, ws=None, n=0, **kw):
+    a = dict(c=cache(), q=rows(), out=rows(), cu=FAKE, kv=FAKE, table=FAKE, stride=4, width=4, batch=2, scale=1.0)
+    a.update(kw)
+    return L().exl3_paged_attention_sinks(B(a["c"]), B(a["q"]), B(a["out"]), a["cu"], a["kv"], a["table"], a["stride"], a["width"],
+                                          a["batch"], tokens, a["scale"], window, sinks, ws, n, None)
+
+
+def prompt_sinks(window=5, sinks=4, tokens=5, **kw):
+    a = dict(q=rows(), k=rows(), v=rows(), out=rows(), cu=FAKE, batch=2, d=128, dtype=1, scale=1.0)
+    a.update(kw)
+    return L().exl3_prompt_attention_sinks(B(a["q"]), B(a["k"]), B(a["v"]), B(a["out"]), a["cu"], a["batch"], tokens, a["d"],
+                                           a["dtype"], window, sinks, a["scale"], None, 0, None)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(window=0), "window=0"), (dict(window=-1), "window=-1"), (dict(window=(1 << 30) + 1), "window="),
+    (dict(sinks=-1), "sinks=-1"), (dict(sinks=(1 << 20) + 1), "sinks=1048577"), (dict(cu=None), "cu"), (dict(batch=0), "batch=0"),
+    (dict(scale=0.0), "scale=0"), (dict(out=rows(3)), "out has 3 heads"), (dict(q=rows(6), out=rows(6)), "multiple of the 4")])
+def test_sinks_refusals(kw, msg):
+    assert paged_sinks(**kw) == 1 and msg in last(), last()
+    assert prompt_sinks(**kw) == 1 and msg in last(), last()
+
+
+def test_sinks_need_the_workspace_that_the_plain_calls_need():
+    need = ex.attention_workspace_bytes(2, 3, 4, 4, 128)
+    assert need > 0 and paged_sinks() == 3 and f"needs {need}" in last()
+    assert paged_sinks(tokens=0) == 0 and prompt_sinks(tokens=0) == 0
