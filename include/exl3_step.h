@@ -88,6 +88,27 @@ exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, 
                                         int32_t head_dim, int32_t dtype, int32_t window, int32_t sinks, float scale,
                                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* exl3_paged_attention (without a window) of sequences that share prefixes.
+ * Group g is the sequences group_cu[g] .. group_cu[g+1]-1 (int32 [groups+1],
+ * non-decreasing, from 0 to batch; at most as many groups as sequences;
+ * sequences of no group share nothing), whose rows of the page table have the same pages for their first prefix_len[g]
+ * (int32 [groups]) keys.  Of those, the keys before every new token of the
+ * group's sequences are read once for all of them, by way of the first one's
+ * row of the table; the result is exl3_paged_attention's but for the order of
+ * sums.  Three launches; one that nothing shares is faster by
+ * exl3_paged_attention.  An offset in group_cu counts as at least those before it
+ * and at most batch. */
+exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
+                                  const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
+                                  int64_t page_table_stride, int32_t page_table_width, int32_t batch, int32_t tokens,
+                                  const int32_t *group_cu, const int32_t *prefix_len, int32_t groups, float scale,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of exl3_prefix_attention, with counters at its start like that of
+ * the other attention calls, which may be the same. */
+size_t exl3_prefix_attention_workspace_bytes(int32_t batch, int32_t tokens, int32_t groups, int32_t q_heads,
+                                             int32_t kv_heads, int32_t head_dim);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,6 +33,7 @@ __all__ = [
     "moe_combine", "moe_forward", "reserve_workspace", "workspace_key",
     "Rope", "KvCache", "split_heads", "rope", "cache_write", "cache_read", "rope_cache_write", "paged_attention",
     "prompt_attention", "attention_workspace_bytes", "HeadNorm", "CacheStep", "cache_extend",
+    "prefix_attention", "prefix_attention_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -684,4 +685,5 @@ def moe_forward(x: torch.Tensor, w: MoeWeight, topk_ids: torch.Tensor, topk_weig
 # Between the projections: rotary positions, the paged cache and attention
 # (over include/exl3_attn.h and exl3_step.h; needs the names above).
 from .attention import (CacheStep, HeadNorm, KvCache, Rope, attention_workspace_bytes, cache_extend, cache_read,  # noqa: E402
-                        cache_write, paged_attention, prompt_attention, rope, rope_cache_write, split_heads)
+                        cache_write, paged_attention, prefix_attention, prefix_attention_workspace_bytes,
+                        prompt_attention, rope, rope_cache_write, split_heads)

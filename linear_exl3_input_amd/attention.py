@@ -38,7 +38,8 @@ import torch
 from . import _BF16, _F16, _HERE, _check, _workspace, _workspaces, _ws_needs_zero, load
 
 __all__ = ["Rope", "KvCache", "split_heads", "rope", "cache_write", "cache_read", "rope_cache_write",
-           "paged_attention", "prompt_attention", "attention_workspace_bytes", "HeadNorm", "CacheStep", "cache_extend"]
+           "paged_attention", "prompt_attention", "attention_workspace_bytes", "HeadNorm", "CacheStep", "cache_extend",
+           "prefix_attention", "prefix_attention_workspace_bytes"]
 
 ATTN_HEADER = os.path.join(os.path.dirname(_HERE), "include", "exl3_attn.h")
 STEP_HEADER = os.path.join(os.path.dirname(_HERE), "include", "exl3_step.h")
@@ -94,6 +95,8 @@ def _lib():
             "exl3_norm_rope_cache_write": (i32, [C, A, N, vp, i64, vp, i32, R, R, R, R, R, vp]),
             "exl3_paged_attention_sinks": (i32, [C, R, R, vp, vp, vp, i64, i32, i32, i32, f32, i32, i32, vp, sz, vp]),
             "exl3_prompt_attention_sinks": (i32, [R, R, R, R, vp, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp]),
+            "exl3_prefix_attention": (i32, [C, R, R, vp, vp, vp, i64, i32, i32, i32, vp, vp, i32, f32, vp, sz, vp]),
+            "exl3_prefix_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
             "exl3_cache_extend": (i32, [i32, i32, vp, vp, i32, vp, i64, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
@@ -610,6 +613,45 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     _check(L.exl3_prompt_attention(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), ctypes.byref(o),
                                    _ints(cu_seqlens, "cu_seqlens", B + 1, q.device), B, T, D, _dtype_id(q.dtype, "q"),
                                    int(causal), _window(window), D ** -0.5 if scale is None else scale, ws, wsn, stream))
+    return out
+
+
+def prefix_attention_workspace_bytes(batch: int, tokens: int, groups: int, q_heads: int, kv_heads: int,
+                                     head_dim: int) -> int:
+    """The workspace of a prefix_attention call of these sizes, e.g. for reserve_workspace before a capture."""
+    L = _lib()
+    n = L.exl3_prefix_attention_workspace_bytes(batch, tokens, groups, q_heads, kv_heads, head_dim)
+    if n == 0 and L.exl3_last_error():
+        _check(1)
+    return n
+
+
+def prefix_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor,
+                     page_table: torch.Tensor, group_cu: torch.Tensor, prefix_len: torch.Tensor,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention of sequences that share prefixes, whose keys and values are read once for all that share them.
+
+    Group g is the sequences group_cu[g]..group_cu[g+1]-1 (int32 [groups+1]); their rows of the page table have the same
+    pages for their first prefix_len[g] keys (int32 [groups]).  Sequences of no group share nothing.  The rest is
+    paged_attention's, and so is the result but for the order of sums."""
+    if _current_device() != cache.device.index:
+        with torch.cuda.device(cache.device):
+            return prefix_attention(cache, q, cu_q, kv_len, page_table, group_cu, prefix_len, scale, out)
+    T, H, D = q.shape
+    B, G = kv_len.shape[0], prefix_len.shape[0]
+    dev = cache.device
+    qr = _cache_rows(cache, q, "q")
+    _page_table(page_table, B, dev)
+    out, o = _out(out, q, "out")
+    L = _lib()
+    need = L.exl3_prefix_attention_workspace_bytes(B, T, G, H, cache.heads, D)
+    stream = _raw_stream(dev.index)
+    ws, wsn = _scratch(need, dev, stream)
+    _check(L.exl3_prefix_attention(cache._ref, ctypes.byref(qr), ctypes.byref(o), _ints(cu_q, "cu_q", B + 1, dev),
+                                   _ints(kv_len, "kv_len", B, dev), page_table.data_ptr(), page_table.stride(0),
+                                   page_table.shape[1], B, T, _ints(group_cu, "group_cu", G + 1, dev),
+                                   _ints(prefix_len, "prefix_len", G, dev), G, D ** -0.5 if scale is None else scale,
+                                   ws, wsn, stream))
     return out
 
 

@@ -26,7 +26,9 @@ ARCH = "gfx950"
 
 SOURCES = ["exl3_host.cpp", "exl3_misc.hip", "exl3_moe.hip", "exl3_rulers.hip", "exl3_noalloc.hip", "gemm_dense.hip", "attn_host.cpp", "attn_rows.hip",
            "attn_norm_rows.hip", "step_host.cpp", "step_tables.hip",
-           "attn_sinks_d64.hip", "attn_sinks_d128.hip", "attn_sinks_d256.hip",
+           "attn_sinks_d64.hip", "attn_sinks_d128.hip", "attn_sinks_d256.hip", "step_groups.hip",
+           "attn_prefix_d64.hip", "attn_prefix_d128.hip", "attn_prefix_d256.hip",
+           "attn_own_d64.hip", "attn_own_d128.hip", "attn_own_d256.hip",
            "attn_d64.hip", "attn_d128.hip", "attn_d256.hip"] + [f"gemm_b{b}.hip" for b in range(1, 9)]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", f"--offload-arch={ARCH}",
@@ -36,7 +38,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", f"--offload-arch={A
 # The attention kernels' scores are matrix products that vector instructions
 # read, so products write VGPRs; left alone, the compiler gives kernels with
 # more than 256 registers a wave AGPR results and copies every one.
-EXTRA = {f"attn_{kind}d{d}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for kind in ("", "sinks_") for d in (64, 128, 256)}
+EXTRA = {f"attn_{kind}d{d}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for kind in ("", "sinks_", "prefix_", "own_") for d in (64, 128, 256)}
 
 
 def _hipcc() -> str:

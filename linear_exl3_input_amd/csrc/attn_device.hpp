@@ -160,6 +160,7 @@ struct Work {
   int q0, q_len;      // the sequence's first query row and their number
   int kv_len;
   int part;           // splits > 1: the part's number among those of all split tiles
+  int first;          // ATTN_OWN: the first key
 };
 
 // Every wave of the workgroup finds the same answer.  Sequence s has
@@ -173,7 +174,7 @@ struct Work {
 template <int R, int KIND = ATTN_PLAIN>
 __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w) {
   struct Seq {
-    int q0, ql, kv, tiles, span;
+    int q0, ql, kv, tiles, span, first;
   };
   // Sequences s0 + lane; `from` is where s0 starts at the earliest, then where
   // the 64 after them do.  An offset below an earlier one counts as that one:
@@ -195,6 +196,10 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
     x.tiles = (int)(((int64_t)x.ql * p.group + R - 1) / R);
     // a tile's rows are at most R tokens; its keys start at a multiple of 32
     x.span = p.kv_len ? min(x.kv, p.table_keys) : x.kv;
+    if constexpr (KIND == ATTN_OWN) {
+      x.first = s < p.batch ? p.start[s] : 0;
+      x.span = max(0, x.span - (x.first & ~31));
+    }
     if (p.window > 0) x.span = min(x.span, p.window + R + 32 + (KIND == ATTN_SINKS ? p.sink_keys : 0));
     return x;
   };
@@ -248,6 +253,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       w.q0 = __builtin_amdgcn_readlane(x.q0, l);
       w.q_len = __builtin_amdgcn_readlane(x.ql, l);
       w.kv_len = __builtin_amdgcn_readlane(x.kv, l);
+      if constexpr (KIND == ATTN_OWN) w.first = __builtin_amdgcn_readlane(x.first, l);
       w.part = w.splits > 1 ? pbase + __builtin_amdgcn_readlane(pincl - parts, l) + at : 0;
       // (lengths that are written while the call runs could make more parts than there is room for)
       return w.splits == 1 || w.part - w.split + w.splits <= p.part_cap;
@@ -268,6 +274,7 @@ struct KeyRange {
   int sinks, sink_end, skip;
 };
 
+template <int KIND = ATTN_PLAIN>
 __device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w, int r0, int r_last) {
   KeyRange k;
   k.shift = w.kv_len - w.q_len;
@@ -276,6 +283,7 @@ __device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w
   k.hi = p.causal ? min(w.kv_len, k.p_last + 1) : w.kv_len;
   if (p.kv_len) k.hi = min(k.hi, p.table_keys);  // past the table everything is a hole
   k.lo = p.window > 0 ? max(0, k.p_first - p.window + 1) : 0;
+  if constexpr (KIND == ATTN_OWN) k.lo = w.first;
   if (w.splits > 1) {
     const int64_t from = (int64_t)(k.lo & ~31) + (int64_t)w.split * w.part_keys;
     k.lo = (int)min<int64_t>(max<int64_t>(from, k.lo), MAX_KEYS);
@@ -311,6 +319,12 @@ __device__ __forceinline__ KeyRange sink_range(const AttnParams &p, const Work &
     k.end = (int)min<int64_t>(from + w.part_keys, k.end);
   }
   return k;
+}
+
+// The state of row r of the tile's sequence.
+__device__ __forceinline__ float *state_row(const AttnParams &p, const Work &w, int r, int head, int D) {
+  const int i = quotient(r, p.by_group), h = r - i * p.group;
+  return p.state + ((int64_t)(w.q0 + i) * (p.heads_kv * p.group) + head * p.group + h) * (STATE_PAD + D);
 }
 
 // ------------------------------------------------- parts of a split tile

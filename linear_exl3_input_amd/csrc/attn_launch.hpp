@@ -100,12 +100,18 @@ struct AttnParams {
   int32_t part_min;           // least keys of a part
   int32_t part_cap;           // parts of a head that `part` and `counters` hold
   int32_t sinks, sink_keys;   // ATTN_SINKS: first keys that stay visible, and that rounded up to whole tiles
+  const int32_t *table_row;   // ATTN_PREFIX: the row of the page table for each sequence (a group of them)
+  const int32_t *start;       // ATTN_OWN: the first key of each sequence, those before being in the state
+  float *state;               // ATTN_PREFIX writes, ATTN_OWN reads: [tokens][q heads] rows of STATE_PAD + D floats
 };
+constexpr int STATE_PAD = 4;  // maximum and sum of a row before its D sums, which stay 16-byte aligned
 
 // What a kernel computes, apart from the head size, the types and the tiles.
 enum AttnKind {
   ATTN_PLAIN = 0,  // a range of keys for each row
   ATTN_SINKS = 1,  // a causal window, and the first keys
+  ATTN_PREFIX = 2, // a range of keys, and what is left for a result goes to the state
+  ATTN_OWN = 3,    // the keys from `start` on, added to the state
 };
 
 // bits: 0 (no cache), 16, 8, 4.
@@ -121,5 +127,8 @@ constexpr int ATTN_TILE_ROWS = 128;
 hipError_t launch_attn_tile(int head_dim, bool bf16, int bits, const AttnParams &p, hipStream_t s);
 // ATTN_SINKS; columns as above, 0: tiles of ATTN_TILE_ROWS.
 hipError_t launch_attn_sinks(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+// ATTN_PREFIX and ATTN_OWN, over a cache.
+hipError_t launch_attn_prefix(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_own(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
 
 }  // namespace exl3

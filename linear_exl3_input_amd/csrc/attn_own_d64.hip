@@ -1,0 +1,6 @@
+// Attention kernels of sequences' own keys, heads of 64 values.
+#define EXL3_HEAD_DIM 64
+#define EXL3_KIND ATTN_OWN
+#define EXL3_PACKED 0
+#define EXL3_LAUNCH launch_attn_own_d64
+#include "attn_kind_instances.hpp"

@@ -166,12 +166,13 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   const int item = workgroup() / p.heads_kv;
   Work w;
   if (!find_work<R, KIND>(p, item, lane, w)) return;
+  if (KIND == ATTN_PREFIX && w.kv_len <= 0) return;  // nothing is shared, nothing reads the state
 
   // ---- the tile's rows and their keys
   const int rows = w.q_len * p.group;
   const int r0 = w.tile * R;
   const int r_last = min(r0 + R, rows) - 1;
-  const KeyRange kr = SINKS ? sink_range<32>(p, w, r0, r_last) : key_range(p, w, r0, r_last);
+  const KeyRange kr = SINKS ? sink_range<32>(p, w, r0, r_last) : key_range<KIND>(p, w, r0, r_last);
   const int lo = kr.lo, hi = kr.hi, p_first = kr.p_first, p_last = kr.p_last, shift = kr.shift;
   const int end = SINKS ? kr.end : hi;
   // the key at place x of the steps
@@ -183,7 +184,8 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 
   // ---- where keys and values lie
   const int ps_mask = (1 << p.cache.page_shift) - 1;
-  const int32_t *table = PAGED ? p.page_table + (int64_t)w.seq * p.table_stride : nullptr;
+  const int32_t *table = PAGED ? p.page_table + (int64_t)(KIND == ATTN_PREFIX ? p.table_row[w.seq] : w.seq) * p.table_stride
+                               : nullptr;
   // lane's keys of a step at k0: first product k0 + 8*(c/4) + c%4 and 4 more,
   // second product k0 + 8*g .. + 7; each within one page (pages hold whole 16s)
   auto page_of = [&](int key) __attribute__((always_inline)) -> int {
@@ -569,6 +571,32 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     };
     put(w.split);
     if (!add_parts(p, w, head, add, put)) return;
+  }
+  if constexpr (KIND == ATTN_PREFIX || KIND == ATTN_OWN) {
+    const int d = DV * (4 * g + wave);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (!live[n] || (KIND == ATTN_OWN && w.first <= 0)) continue;
+      float *y = state_row(p, w, r0 + 16 * n + c, head, D);
+      if constexpr (KIND == ATTN_PREFIX) {
+        if (wave == 0 && g == 0) *(float2_t *)y = (float2_t){top[n], total[n]};
+#pragma unroll
+        for (int j = 0; j < DV; j += 4)
+          *(float4_t *)(y + STATE_PAD + d + j) = (float4_t){mine[n][j], mine[n][j + 1], mine[n][j + 2], mine[n][j + 3]};
+      } else {
+        const float2_t ml = *(const float2_t *)y;
+        const float grown = __builtin_fmaxf(top[n], ml.x), base = grown == -INFINITY ? 0.f : grown;
+        const float keep = __builtin_amdgcn_exp2f(top[n] - base), more = __builtin_amdgcn_exp2f(ml.x - base);
+        total[n] = total[n] * keep + ml.y * more;
+#pragma unroll
+        for (int j = 0; j < DV; j += 4) {
+          const float4_t x = *(const float4_t *)(y + STATE_PAD + d + j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mine[n][j + i] = mine[n][j + i] * keep + x[i] * more;
+        }
+      }
+    }
+    if constexpr (KIND == ATTN_PREFIX) return;
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n)

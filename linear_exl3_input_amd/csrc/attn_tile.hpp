@@ -105,6 +105,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int item = workgroup() / p.heads_kv;
   Work w;
   if (!find_work<R, KIND>(p, item, lane, w)) return;
+  if (KIND == ATTN_PREFIX && w.kv_len <= 0) return;  // nothing is shared, nothing reads the state
   const int rows = w.q_len * p.group;
   {
     // a sequence's last tiles have the most keys and go first
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   // ---- the tile's rows and their keys
   const int r0 = w.tile * R;
   const int r_last = min(r0 + R, rows) - 1;
-  const KeyRange kr = SINKS ? sink_range<BN>(p, w, r0, r_last) : key_range(p, w, r0, r_last);
+  const KeyRange kr = SINKS ? sink_range<BN>(p, w, r0, r_last) : key_range<KIND>(p, w, r0, r_last);
   const int lo = kr.lo, hi = kr.hi, p_first = kr.p_first, p_last = kr.p_last, shift = kr.shift;
   const int start = kr.start;
   const int n_tiles = SINKS ? max(0, kr.end - start + BN - 1) / BN : hi > lo ? (hi - start + BN - 1) / BN : 0;
@@ -174,7 +175,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int ka = 4 * (tid / NC), va = 8 * (tid / (2 * NC));
   const int half = (tid / NC) & 1;
   const int ps_mask = (1 << p.cache.page_shift) - 1;
-  const int32_t *table = PAGED ? p.page_table + (int64_t)w.seq * p.table_stride : nullptr;
+  const int32_t *table = PAGED ? p.page_table + (int64_t)(KIND == ATTN_PREFIX ? p.table_row[w.seq] : w.seq) * p.table_stride
+                               : nullptr;
   auto page_of = [&](int key) __attribute__((always_inline)) -> int {
     const int i = key >> p.cache.page_shift;
     int pg = -1;
@@ -639,6 +641,39 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     };
     put(w.split);
     if (!add_parts(p, w, head, add, put)) return;
+  }
+  if constexpr (KIND == ATTN_PREFIX || KIND == ATTN_OWN) {
+    if (row < rows && (KIND == ATTN_PREFIX || w.first > 0)) {
+      float *y = state_row(p, w, row, head, D);
+      float keep = 1.f, more = 0.f;
+      if constexpr (KIND == ATTN_PREFIX) {
+        if (h == 0) *(float2_t *)y = (float2_t){m, l};
+      } else {
+        const float2_t ml = *(const float2_t *)y;
+        const float grown = __builtin_fmaxf(m, ml.x), base = grown == -INFINITY ? 0.f : grown;
+        keep = __builtin_amdgcn_exp2f(m - base), more = __builtin_amdgcn_exp2f(ml.x - base);
+        l = l * keep + ml.y * more;
+      }
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        float4_t *at = (float4_t *)(y + STATE_PAD + 8 * piece_of(x, h));
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          if constexpr (KIND == ATTN_PREFIX) {
+            at[j / 4] = (float4_t){o[prod(j)][elem(x, j)], o[prod(j + 1)][elem(x, j + 1)], o[prod(j + 2)][elem(x, j + 2)],
+                                   o[prod(j + 3)][elem(x, j + 3)]};
+          } else {
+            const float4_t v = at[j / 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int d = prod(j + i), e = elem(x, j + i);
+              o[d][e] = o[d][e] * keep + v[i] * more;
+            }
+          }
+        }
+      }
+    }
+    if constexpr (KIND == ATTN_PREFIX) return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key is zero
   int ln = lane;

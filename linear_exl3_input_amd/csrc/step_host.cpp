@@ -94,9 +94,50 @@ exl3_status run_sinks(AttnParams &p, int32_t head_dim, bool bf16, int32_t bits, 
                        [&](int columns) { return launch_attn_sinks(head_dim, bf16, bits, p, columns, s); });
 }
 
+// The workspace of a call with shared prefixes: the counters, the parts of
+// either pass, what the groups are, and the state of every row.
+struct PrefixPlan {
+  AttnPlan shared, own;  // the groups as sequences; the sequences
+  size_t ints, state, workspace;  // offsets
+};
+
+exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q_heads, int32_t kv_heads,
+                        int32_t head_dim, PrefixPlan *pl) {
+  exl3_status st;
+  if (groups < 0 || groups > batch)
+    return host_fail(EXL3_ERR_INVALID_ARG, "groups=%d, must be 0..batch=%d", groups, batch);
+  if ((st = plan_attention(batch, tokens, q_heads, kv_heads, head_dim, &pl->own)) != EXL3_OK) return st;
+  if ((st = plan_attention(groups, tokens, q_heads, kv_heads, head_dim, &pl->shared)) != EXL3_OK) return st;
+  auto whole = [](size_t n) { return (n + 255) & ~(size_t)255; };
+  pl->ints = whole(std::max({pl->own.workspace, pl->shared.workspace, (size_t)EXL3_WORKSPACE_COUNTER_BYTES}));
+  pl->state = pl->ints + whole(sizeof(int32_t) * (2 * (size_t)batch + 1 + 3 * (size_t)groups + 2));
+  pl->workspace = pl->state + sizeof(float) * (size_t)tokens * q_heads * (STATE_PAD + head_dim);
+  return EXL3_OK;
+}
+
 }  // namespace
 
 namespace exl3 {
+
+hipError_t launch_attn_prefix_d64(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_prefix_d128(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_prefix_d256(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+
+hipError_t launch_attn_prefix(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s) {
+  return head_dim == 64    ? launch_attn_prefix_d64(bf16, bits, p, columns, s)
+         : head_dim == 128 ? launch_attn_prefix_d128(bf16, bits, p, columns, s)
+                           : launch_attn_prefix_d256(bf16, bits, p, columns, s);
+}
+
+hipError_t launch_attn_own_d64(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_own_d128(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_own_d256(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+
+hipError_t launch_attn_own(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s) {
+  return head_dim == 64    ? launch_attn_own_d64(bf16, bits, p, columns, s)
+         : head_dim == 128 ? launch_attn_own_d128(bf16, bits, p, columns, s)
+                           : launch_attn_own_d256(bf16, bits, p, columns, s);
+}
 
 hipError_t launch_attn_sinks_d64(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
 hipError_t launch_attn_sinks_d128(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
@@ -261,6 +302,61 @@ exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, 
   if (st != EXL3_OK || tokens == 0) return st;
   return run_sinks(p, head_dim, dtype == EXL3_BF16, 0, q->heads, sinks, workspace, workspace_bytes,
                    (hipStream_t)stream);
+}
+
+size_t exl3_prefix_attention_workspace_bytes(int32_t batch, int32_t tokens, int32_t groups, int32_t q_heads,
+                                             int32_t kv_heads, int32_t head_dim) {
+  host_clear_error();
+  PrefixPlan pl;
+  if (check_shape(tokens, head_dim, EXL3_BF16) != EXL3_OK) return 0;
+  if (check_attention_sizes(batch, tokens, q_heads, kv_heads) != EXL3_OK) return 0;
+  if (plan_prefix(batch, tokens, groups, q_heads, kv_heads, head_dim, &pl) != EXL3_OK) return 0;
+  return pl.workspace;
+}
+
+exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
+                                  const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
+                                  int64_t page_table_stride, int32_t page_table_width, int32_t batch, int32_t tokens,
+                                  const int32_t *group_cu, const int32_t *prefix_len, int32_t groups, float scale,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+  host_clear_error();
+  AttnParams p;
+  exl3_status st = paged_params(p, c, q, out, cu_q, kv_len, page_table, page_table_stride, page_table_width, batch,
+                                tokens, scale, 0);
+  if (st != EXL3_OK) return st;
+  const int32_t D = c->head_dim;
+  PrefixPlan pl;
+  if ((st = plan_prefix(batch, tokens, groups, q->heads, c->heads, D, &pl)) != EXL3_OK) return st;
+  if (tokens == 0) return EXL3_OK;
+  if ((st = check_ints(group_cu, "group_cu")) != EXL3_OK) return st;
+  if (groups > 0 && (st = check_ints(prefix_len, "prefix_len")) != EXL3_OK) return st;
+  if (workspace == nullptr || workspace_bytes < pl.workspace)
+    return host_fail(EXL3_ERR_WORKSPACE, "workspace of %zu bytes; this call needs %zu (short by %zu)", workspace_bytes,
+                     pl.workspace, pl.workspace > workspace_bytes ? pl.workspace - workspace_bytes : (size_t)0);
+  if ((st = check_ptr(workspace, "workspace")) != EXL3_OK) return st;
+  const hipStream_t s = (hipStream_t)stream;
+  const bool bf16 = c->dtype == EXL3_BF16;
+  char *ws = static_cast<char *>(workspace);
+  int32_t *ints = reinterpret_cast<int32_t *>(ws + pl.ints);
+  const GroupsParams g = {cu_q,       kv_len, group_cu,     prefix_len,       batch,
+                          tokens,     groups, p.table_keys, ints,             ints + batch + 1,
+                          ints + 2 * batch + 1, ints + 2 * batch + 1 + groups + 1, ints + 2 * batch + 1 + 2 * (groups + 1)};
+  if ((st = launched(launch_groups(g, s), "groups launch")) != EXL3_OK) return st;
+  p.state = reinterpret_cast<float *>(ws + pl.state);
+  if (groups > 0) {
+    AttnParams shared = p;
+    shared.cu = g.row;
+    shared.kv_len = g.keys;
+    shared.table_row = g.first;
+    shared.batch = groups;
+    shared.causal = 0;
+    st = run_attention(shared, D, q->heads, workspace, workspace_bytes,
+                       [&](int columns) { return launch_attn_prefix(D, bf16, c->bits, shared, columns, s); });
+    if (st != EXL3_OK) return st;
+  }
+  p.start = g.start;
+  return run_attention(p, D, q->heads, workspace, workspace_bytes,
+                       [&](int columns) { return launch_attn_own(D, bf16, c->bits, p, columns, s); });
 }
 
 }  // extern "C"

@@ -21,4 +21,18 @@ struct TablesParams {
 
 hipError_t launch_tables(const TablesParams &p, hipStream_t s);
 
+// What the two passes of attention with shared prefixes need of the groups.
+struct GroupsParams {
+  const int32_t *cu, *kv_len;            // [batch+1], [batch]
+  const int32_t *group_cu, *prefix_len;  // [groups+1], [groups]
+  int32_t batch, tokens, groups, table_keys;
+  int32_t *seq_row;                      // [batch+1] the first row of each sequence
+  int32_t *start;                        // [batch] the first key that is not shared
+  int32_t *first;                        // [groups+1] the first sequence of each group
+  int32_t *row;                          // [groups+1] the first row of each group
+  int32_t *keys;                         // [groups] its shared keys
+};
+
+hipError_t launch_groups(const GroupsParams &p, hipStream_t s);
+
 }  // namespace exl3

@@ -212,3 +212,34 @@ def test_sinks_need_the_workspace_that_the_plain_calls_need():
     need = ex.attention_workspace_bytes(2, 3, 4, 4, 128)
     assert need > 0 and paged_sinks() == 3 and f"needs {need}" in last()
     assert paged_sinks(tokens=0) == 0 and prompt_sinks(tokens=0) == 0
+
+
+# ------------------------------------------------------- shared prefixes
+
+def prefix(tokens=3, groups=1, group_cu=FAKE, lens=FAKE, ws=None, n=0, **kw):
+    a = dict(c=cache(), q=rows(), out=rows(), cu=FAKE, kv=FAKE, table=FAKE, stride=4, width=4, batch=2, scale=1.0)
+    a.update(kw)
+    return L().exl3_prefix_attention(B(a["c"]), B(a["q"]), B(a["out"]), a["cu"], a["kv"], a["table"], a["stride"], a["width"],
+                                     a["batch"], tokens, group_cu, lens, groups, a["scale"], ws, n, None)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(groups=-1), "groups=-1"), (dict(groups=3), "groups=3, must be 0..batch=2"), (dict(group_cu=None), "group_cu is NULL"),
+    (dict(lens=None), "prefix_len is NULL"), (dict(lens=FAKE + 2), "not 4-byte aligned"), (dict(cu=None), "cu"), (dict(batch=0), "batch=0"),
+    (dict(scale=-1.0), "scale=-1"), (dict(out=rows(3)), "out has 3 heads"), (dict(q=rows(6), out=rows(6)), "multiple of the 4"),
+    (dict(kv=None), "kv_len is NULL"), (dict(stride=-4), "negative")])
+def test_prefix_refusals(kw, msg):
+    assert prefix(**kw) == 1 and msg in last(), last()
+
+
+def test_prefix_workspace():
+    need = ex.prefix_attention_workspace_bytes(2, 3, 1, 4, 4, 128)
+    state = 3 * 4 * 132 * 4
+    assert need >= ex.attention_workspace_bytes(2, 3, 4, 4, 128) + state and need >= ex.attention_workspace_bytes(1, 3, 4, 4, 128) + state
+    for ws, n in ((None, need), (FAKE, need - 1), (FAKE, 0)):
+        assert prefix(ws=ws, n=n) == 3 and f"needs {need}" in last()
+    assert prefix(ws=FAKE + 4, n=need) == 1 and "not 16-byte aligned" in last()
+    assert prefix(tokens=0) == 0 and prefix(tokens=0, groups=0, group_cu=None, lens=None) == 0
+    for args in ((-1, 1, 0, 4, 4, 128), (1, 1, 2, 4, 4, 128), (1, 1, -1, 4, 4, 128), (1, 1, 1, 5, 4, 128), (1, 1, 1, 4, 4, 100)):
+        with pytest.raises(ex.Exl3Error):
+            ex.prefix_attention_workspace_bytes(*args)
