@@ -67,6 +67,7 @@ struct NormRowsParams {
   const float *wq, *wk;      // null: not normed; weights of the heads' dims
   int32_t wq_step, wk_step;  // from one head's weights to the next's: 0 or the head size
   float eps;
+  Divisor by_units;          // waves of a token (set by the launcher)
 };
 
 struct ReadParams {

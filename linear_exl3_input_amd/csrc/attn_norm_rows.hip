@@ -10,6 +10,14 @@ namespace exl3 {
 // the type at the end.  As in rows_kernel a row is D/8 lanes of one wave with 8
 // consecutive values each; the sum of squares goes over those lanes by lane
 // moves, and a lane loads its pairs' other halves too where they are rot/2 away.
+//
+// What bounds it: bytes, with the vector units not far behind (with a row for
+// every D/8 lanes and all of the look-up done by lanes, 105 us on the first
+// below, 420 vector instructions a wave of two rows, 70% of the cycles; 67 with
+// coefficients for several rows; 64 with the look-up as scalar work).
+// Measured: 12001 tokens normed, rotated and written to 8 bits, 32/8 heads of
+// 128, 270 MB in 64 us, 4.2 TB/s (a copy reaches 4.97); 9973 tokens over three
+// axes, 209 MB in 47 us, 4.4 TB/s; 16 tokens, 24/4 heads of 256, 3.1 us.
 template <int D>
 __device__ __forceinline__ float row_sum(float v) {
   v += lane_xor<1>(v);
@@ -38,65 +46,80 @@ __device__ __forceinline__ void load_floats(const float *a, float (&f)[8]) {
   for (int i = 0; i < 4; ++i) f[i] = x[i], f[4 + i] = y[i];
 }
 
-// 1 / the root mean square of a row, given the lane's 8 values.  Squares of
-// bfloat16 values past 2^64 are infinite; such a row is summed again scaled
-// down (its eps counts nothing).
+// Of a row's 8 values a lane: 1 / the root of their mean square plus eps.
+// Squares of bfloat16 values past 2^64 are infinite; the values of such a row
+// are scaled down first, here and in f and g (its eps counts nothing then).
 template <int D>
-__device__ __forceinline__ float inverse_rms(const float (&f)[8], float eps) {
+__device__ __forceinline__ float inverse_rms(float (&f)[8], float (&g)[8], float eps) {
   float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
+  for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
   ss = row_sum<D>(ss);
-  if (ss < INFINITY) return __builtin_amdgcn_rsqf(ss * (1.f / D) + eps);
+  if (ss < INFINITY) return __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.f / D, eps));
   ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float g = f[i] * 0x1p-70f;
-    ss += g * g;
+    f[i] *= 0x1p-70f;
+    g[i] *= 0x1p-70f;
+    ss = __builtin_fmaf(f[i], f[i], ss);
   }
-  return __builtin_amdgcn_rsqf(row_sum<D>(ss) * (1.f / D)) * 0x1p-70f;
+  return __builtin_amdgcn_rsqf(row_sum<D>(ss) * (1.f / D));
 }
 
-template <bool BF16, int D, int BITS, bool NORM, bool AXES>
+// A wave has one token and up to 512 / D * HB of its query heads, key heads or
+// values: all that is looked up by token, kind and number of heads is then
+// scalar work.  What a lane multiplies its values f and their partners g by,
+// y = f * A + g * B, depends on the token and the weights alone, so cosines,
+// sines and weights are read and multiplied once for HB rows (with norms y is
+// multiplied by the row's 1 / rms).
+template <bool BF16, int D, int BITS, bool NORM, bool AXES, int HB>
 __global__ __launch_bounds__(256) void norm_rows_kernel(NormRowsParams np) {
   const RowsParams &p = np.rows;
-  constexpr int LPR = D / 8;  // lanes per row
-  const int c = threadIdx.x % LPR;
-  const int64_t row = (int64_t)workgroup() * (256 / LPR) + threadIdx.x / LPR;
-  const int H = p.hq + p.hk + p.hv;
-  if (row >= (int64_t)p.tokens * H) return;  // whole rows leave: the lane moves stay within rows
-  const uint32_t t = (uint32_t)row / (uint32_t)H;
-  int h = (int)((uint32_t)row - t * (uint32_t)H);
-  const bool is_q = h < p.hq, is_v = h >= p.hq + p.hk;
-  const Rows src = is_q ? p.q : is_v ? p.v : p.k;
-  h -= is_q ? 0 : is_v ? p.hq + p.hk : p.hq;
-  const uint16_t *x = src.data + (int64_t)t * src.token + (int64_t)h * src.head;
-  u32x4_t own = *(const u32x4_t *)(x + 8 * c);
-  uint32_t w[4] = {own.x, own.y, own.z, own.w};
-  if (!is_v) {
-    float f[8];
-    eight_floats<BF16>(own, f);
-    float inv = 1.f;
-    const float *weight = nullptr;
-    if constexpr (NORM) {
-      inv = inverse_rms<D>(f, np.eps);
-      weight = is_q ? np.wq + (int64_t)h * np.wq_step : np.wk + (int64_t)h * np.wk_step;
-      float g[8];
-      load_floats(weight + 8 * c, g);
+  constexpr int LPR = D / 8;     // lanes per row
+  constexpr int RPW = 64 / LPR;  // rows side by side
+  const int lane = threadIdx.x & 63, c = lane % LPR;
+  const int uq = (p.hq + RPW * HB - 1) / (RPW * HB), uk = (p.hk + RPW * HB - 1) / (RPW * HB),
+            uv = (p.hv + RPW * HB - 1) / (RPW * HB);
+  const int wave = __builtin_amdgcn_readfirstlane(workgroup() * 4 + (threadIdx.x >> 6));
+  const int t = quotient(wave, np.by_units);
+  if (t >= p.tokens) return;
+  int u = wave - t * (uq + uk + uv);
+  const bool is_q = u < uq, is_v = u >= uq + uk;
+  // (members one by one: a choice between structs puts the arguments into memory)
+  auto pick = [&](auto q, auto k, auto v) __attribute__((always_inline)) { return is_q ? q : is_v ? v : k; };
+  const int64_t row_step = pick(p.q.head, p.k.head, p.v.head);
+  const int heads = pick(p.hq, p.hk, p.hv);
+  u -= is_q ? 0 : is_v ? uq + uk : uq;
+  const int h0 = u * RPW * HB + lane / LPR;  // the lane's heads h0, h0 + RPW, ...
+  const uint16_t *x = pick(p.q.data, p.k.data, p.v.data) + (int64_t)t * pick(p.q.token, p.k.token, p.v.token);
+  const int half = p.rot >> 1;
+  const bool turns = !is_v && 8 * c < p.rot;
+  const bool second = !p.interleaved && 8 * c >= half;  // this lane holds the b of its pairs
+  const int i0 = p.interleaved ? 4 * c : second ? 8 * c - half : 8 * c;  // the lane's first pair
+  const int o0 = second ? i0 : i0 + half;                                // and its values' partners
+  u32x4_t own[HB], other[HB];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * g[i];
-    }
-    uint32_t nan = 0;  // values whose position is none
-    if (8 * c < p.rot) {
-      const int half = p.rot >> 1;
-      const bool second = !p.interleaved && 8 * c >= half;  // this lane holds the b of its pairs
-      const int i0 = p.interleaved ? 4 * c : second ? 8 * c - half : 8 * c;  // the lane's first pair
+  for (int i = 0; i < HB; ++i) {
+    const uint16_t *row = x + (int64_t)min(h0 + i * RPW, heads - 1) * row_step;
+    own[i] = *(const u32x4_t *)(row + 8 * c);
+    other[i] = (u32x4_t){0u, 0u, 0u, 0u};
+    if (turns && !p.interleaved) other[i] = *(const u32x4_t *)(row + o0);
+  }
+  float A[8], B[8];
+  uint32_t nan = 0;  // values whose position is none
+  if (!is_v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) A[i] = 1.f, B[i] = 0.f;
+    if (turns) {
       float co[8], si[8];
       if constexpr (AXES) {
         int32_t at[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a) at[a] = a < np.axes ? p.positions[a * np.axis_stride + t] : 0;
-        const uint32_t word = np.axis_of[i0 >> 4] >> (2 * (i0 & 15));
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) word = i0 >> 4 == i ? np.axis_of[i] : word;
+        word >>= 2 * (i0 & 15);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (p.interleaved && i >= 4) break;
@@ -119,73 +142,119 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormRowsParams np) {
         }
         nan = known ? 0u : 0xFFu;
       }
+      // a' = a*cos - b*sin, b' = b*cos + a*sin
       if (p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float a = f[2 * i], b = f[2 * i + 1];
-          f[2 * i] = a * co[i] - b * si[i];
-          f[2 * i + 1] = b * co[i] + a * si[i];
+          A[2 * i] = A[2 * i + 1] = co[i];
+          B[2 * i] = -si[i], B[2 * i + 1] = si[i];
         }
       } else {
-        const int o0 = second ? i0 : i0 + half;
-        float g[8];
-        eight_floats<BF16>(*(const u32x4_t *)(x + o0), g);
-        if constexpr (NORM) {
-          float gw[8];
-          load_floats(weight + o0, gw);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = g[i] * inv * gw[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f[i] * co[i] + g[i] * (second ? si[i] : -si[i]);  // a*cos - b*sin, or b*cos + a*sin
+        for (int i = 0; i < 8; ++i) A[i] = co[i], B[i] = second ? si[i] : -si[i];
       }
     }
-    if (NORM || 8 * c < p.rot) {
+    if constexpr (NORM) {
+      const int hw = min(h0, heads - 1);
+      const float *weight = is_q ? np.wq + (int64_t)hw * np.wq_step : np.wk + (int64_t)hw * np.wk_step;
+      float w[8];
+      load_floats(weight + 8 * c, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = Half<BF16>::pack(f[2 * i], f[2 * i + 1]);
-        if (nan != 0) {
-          constexpr uint32_t QUIET = BF16 ? 0x7FC0u : 0x7E00u;
-          if ((nan >> (2 * i)) & 1u) w[i] = (w[i] & 0xFFFF0000u) | QUIET;
-          if ((nan >> (2 * i)) & 2u) w[i] = (w[i] & 0xFFFFu) | QUIET << 16;
-        }
+      for (int i = 0; i < 8; ++i) A[i] *= w[i];
+      if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) B[i] *= w[i ^ 1];
+      } else if (turns) {
+        load_floats(weight + o0, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) B[i] *= w[i];
       }
     }
   }
-  const u32x4_t res = {w[0], w[1], w[2], w[3]};
-  if (is_q) {
-    *(u32x4_t *)(p.q_out.data + (int64_t)t * p.q_out.token + (int64_t)h * p.q_out.head + 8 * c) = res;
-    return;
-  }
-  if (!is_v && p.k_out.data != nullptr)
-    *(u32x4_t *)(p.k_out.data + (int64_t)t * p.k_out.token + (int64_t)h * p.k_out.head + 8 * c) = res;
+  int32_t slot_at = -1;
   if constexpr (BITS != 0) {
-    const int32_t slot = p.slots[t];
-    const int32_t page = slot >> p.cache.page_shift;
-    if (slot < 0 || page >= p.cache.pages) return;
-    const int off = slot & ((1 << p.cache.page_shift) - 1);
-    const int64_t r = ((int64_t)h << p.cache.page_shift) + off;  // the row within its page
-    uint8_t *codes = is_v ? p.cache.v + page * p.cache.v_page : p.cache.k + page * p.cache.k_page;
-    uint8_t *scales = BITS == 16 ? nullptr : is_v ? p.cache.v_scale + page * p.cache.vs_page
-                                                  : p.cache.k_scale + page * p.cache.ks_page;
-    write_codes<BF16, D, BITS>(w, codes + r * (D * BITS / 8), BITS == 16 ? nullptr : scales + r * (D / 32), c);
+    if (!is_q) slot_at = p.slots[t];
+  }
+#pragma unroll
+  for (int i = 0; i < HB; ++i) {
+    const int h = h0 + i * RPW;
+    if (u * RPW * HB + i * RPW >= heads) break;
+    uint32_t w[4] = {own[i].x, own[i].y, own[i].z, own[i].w};
+    if (!is_v && (NORM || turns)) {
+      float f[8], g[8];
+      eight_floats<BF16>(own[i], f);
+      if (p.interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = f[j ^ 1];
+      } else {
+        eight_floats<BF16>(other[i], g);
+      }
+      if constexpr (NORM) {
+        const float inv = inverse_rms<D>(f, g, np.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __builtin_fmaf(f[j], A[j], g[j] * B[j]) * inv;
+      } else {  // rounded as rows_kernel does
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f[j] * A[j] + g[j] * B[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = Half<BF16>::pack(f[2 * j], f[2 * j + 1]);
+      if (nan != 0) {
+        constexpr uint32_t QUIET = BF16 ? 0x7FC0u : 0x7E00u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if ((nan >> (2 * j)) & 1u) w[j] = (w[j] & 0xFFFF0000u) | QUIET;
+          if ((nan >> (2 * j)) & 2u) w[j] = (w[j] & 0xFFFFu) | QUIET << 16;
+        }
+      }
+    }
+    if (h >= heads) continue;  // whole rows: the lane moves stay within rows
+    const u32x4_t res = {w[0], w[1], w[2], w[3]};
+    if (is_q) {
+      *(u32x4_t *)(p.q_out.data + (int64_t)t * p.q_out.token + (int64_t)h * p.q_out.head + 8 * c) = res;
+      continue;
+    }
+    if (!is_v && p.k_out.data != nullptr)
+      *(u32x4_t *)(p.k_out.data + (int64_t)t * p.k_out.token + (int64_t)h * p.k_out.head + 8 * c) = res;
+    if constexpr (BITS != 0) {
+      const int32_t page = slot_at >> p.cache.page_shift;
+      if (slot_at < 0 || page >= p.cache.pages) continue;
+      const int off = slot_at & ((1 << p.cache.page_shift) - 1);
+      const int64_t r = ((int64_t)h << p.cache.page_shift) + off;  // the row within its page
+      uint8_t *codes = is_v ? p.cache.v + page * p.cache.v_page : p.cache.k + page * p.cache.k_page;
+      uint8_t *scales = BITS == 16 ? nullptr : is_v ? p.cache.v_scale + page * p.cache.vs_page
+                                                    : p.cache.k_scale + page * p.cache.ks_page;
+      write_codes<BF16, D, BITS>(w, codes + r * (D * BITS / 8), BITS == 16 ? nullptr : scales + r * (D / 32), c);
+    }
   }
 }
 
 namespace {
 
+template <bool BF16, int D, int BITS, int HB>
+hipError_t norm_rows_heads(NormRowsParams p, hipStream_t s) {
+  constexpr int PER = 512 / D * HB;  // heads of a wave
+  auto units = [](int heads) { return (heads + PER - 1) / PER; };
+  const int each = units(p.rows.hq) + units(p.rows.hk) + units(p.rows.hv);
+  p.by_units = Divisor::of((uint32_t)each);
+  const dim3 grid = grid_of(((int64_t)p.rows.tokens * each + 3) / 4), block(256);
+  if (p.wq == nullptr)
+    hipLaunchKernelGGL((norm_rows_kernel<BF16, D, BITS, false, true, HB>), grid, block, 0, s, p);
+  else if (p.axes > 1)
+    hipLaunchKernelGGL((norm_rows_kernel<BF16, D, BITS, true, true, HB>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((norm_rows_kernel<BF16, D, BITS, true, false, HB>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
 template <bool BF16, int D, int BITS>
 hipError_t norm_rows_of(const NormRowsParams &p, hipStream_t s) {
-  constexpr int RPB = 256 / (D / 8);
-  const int64_t rows = (int64_t)p.rows.tokens * (p.rows.hq + p.rows.hk + p.rows.hv);
-  const dim3 grid = grid_of((rows + RPB - 1) / RPB), block(256);
-  if (p.wq == nullptr)
-    hipLaunchKernelGGL((norm_rows_kernel<BF16, D, BITS, false, true>), grid, block, 0, s, p);
-  else if (p.axes > 1)
-    hipLaunchKernelGGL((norm_rows_kernel<BF16, D, BITS, true, true>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((norm_rows_kernel<BF16, D, BITS, true, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+  // Two rows a lane once there are waves enough for it: 32/8/8 heads of 128 in
+  // one / two rows a lane, 200 tokens 4.2 / 4.1 us, 500 5.7 / 5.5, 12001 77.7 /
+  // 63.7 (four: 4.8, 5.5, 61.7, but over three axes 56.0 where two take 47.2).
+  const int64_t waves = (int64_t)p.rows.tokens * (p.rows.hq + p.rows.hk + p.rows.hv) * (D / 8) / 64;
+  const bool shared = p.wq_step == 0 && p.wk_step == 0;  // the heads of a lane have the same weights
+  return shared && waves >= 4096 ? norm_rows_heads<BF16, D, BITS, 2>(p, s) : norm_rows_heads<BF16, D, BITS, 1>(p, s);
 }
 
 template <bool BF16, int D>
