@@ -95,8 +95,8 @@ exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, 
  * (int32 [groups]) keys.  Of those, the keys before every new token of the
  * group's sequences are read once for all of them, by way of the first one's
  * row of the table; the result is exl3_paged_attention's but for the order of
- * sums.  Three launches; one that nothing shares is faster by
- * exl3_paged_attention.  An offset in group_cu counts as at least those before it
+ * sums.  Calls that gain nothing by it, by their sizes (few sequences or a narrow
+ * page table), are one launch of that, others three.  An offset in group_cu counts as at least those before it
  * and at most batch. */
 exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
                                   const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,

@@ -227,17 +227,26 @@ inline exl3_status check_attention_sizes(int32_t batch, int32_t tokens, int32_t 
   return EXL3_OK;
 }
 
-// The kernel and the split of a call, from its sizes alone.
-inline exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                           AttnPlan *pl) {
+// Rows of a tile: of a workgroup of the small kernel, or (columns 0) the tile kernel.
+inline int32_t tile_rows(int32_t columns) { return columns == 0 ? ATTN_TILE_ROWS : 16 * columns; }
+
+// The kernel for sequences of that many rows on a key/value head on average.
+inline int32_t plan_columns(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   const int32_t group = q_heads / kv_heads;
-  const double rows = batch > 0 ? (double)tokens * group / batch : 0.0;  // a sequence's, on one key/value head
-  pl->columns = rows > tile_min_rows(batch, kv_heads, head_dim) ? 0 : rows > 16.0 && head_dim < 256 ? 2 : 1;
+  const double rows = batch > 0 ? (double)tokens * group / batch : 0.0;
+  return rows > tile_min_rows(batch, kv_heads, head_dim) ? 0 : rows > 16.0 && head_dim < 256 ? 2 : 1;
+}
+
+// The split of a call's keys with a kernel, from its sizes alone.
+inline exl3_status plan_split(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                              int32_t columns, AttnPlan *pl) {
+  const int32_t group = q_heads / kv_heads;
+  pl->columns = columns;
   pl->target = 0;
   pl->workspace = 0;
   const bool tile = pl->columns == 0;
   pl->part_min = tile ? TILE_PART_MIN : PART_MIN;
-  const int32_t R = tile ? ATTN_TILE_ROWS : 16 * pl->columns;
+  const int32_t R = tile_rows(columns);
   const int64_t tiles = (int64_t)tokens * group / R + batch;  // at most, on each key/value head
   const int64_t per_cu = (tile ? head_dim == 256 : head_dim * pl->columns >= 256) ? 1 : 2;  // workgroups of a round
   const int64_t round = per_cu * host_cus();
@@ -254,6 +263,12 @@ inline exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads
   if (items * kv_heads > MAX_GRID)
     return host_fail(EXL3_ERR_UNSUPPORTED, "%d tokens x %d heads: more tiles than a launch holds", tokens, q_heads);
   return EXL3_OK;
+}
+
+inline exl3_status plan_attention(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                  AttnPlan *pl) {
+  return plan_split(batch, tokens, q_heads, kv_heads, head_dim,
+                    plan_columns(batch, tokens, q_heads, kv_heads, head_dim), pl);
 }
 
 // The checks of a call over the cache, and its parameters but for what run_attention
@@ -347,18 +362,15 @@ inline exl3_status prompt_params(AttnParams &p, const exl3_rows *q, const exl3_r
   return EXL3_OK;
 }
 
-// Launches by launch(columns), the tile kernel's columns being 0.
+// Launches a planned call by launch(columns), the tile kernel's columns being 0.
 template <class Launch>
-exl3_status run_attention(AttnParams &p, int32_t head_dim, int32_t q_heads, void *workspace, size_t workspace_bytes,
-                          Launch launch) {
-  AttnPlan pl;
-  exl3_status st = plan_attention(p.batch, p.tokens, q_heads, p.heads_kv, head_dim, &pl);
-  if (st != EXL3_OK) return st;
+exl3_status run_planned(AttnParams &p, const AttnPlan &pl, void *workspace, size_t workspace_bytes, Launch launch) {
   if (pl.workspace > 0) {
     if (workspace == nullptr || workspace_bytes < pl.workspace)
       return host_fail(EXL3_ERR_WORKSPACE, "workspace of %zu bytes; this call needs %zu (short by %zu)", workspace_bytes,
                        pl.workspace, pl.workspace > workspace_bytes ? pl.workspace - workspace_bytes : (size_t)0);
-    if ((st = check_ptr(workspace, "workspace")) != EXL3_OK) return st;
+    const exl3_status st = check_ptr(workspace, "workspace");
+    if (st != EXL3_OK) return st;
     p.counters = static_cast<uint32_t *>(workspace);
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + EXL3_WORKSPACE_COUNTER_BYTES);
   }
@@ -366,6 +378,14 @@ exl3_status run_attention(AttnParams &p, int32_t head_dim, int32_t q_heads, void
   p.part_min = pl.part_min;
   p.part_cap = pl.part_cap;
   return launched(launch(pl.columns), "attention launch");
+}
+
+template <class Launch>
+exl3_status run_attention(AttnParams &p, int32_t head_dim, int32_t q_heads, void *workspace, size_t workspace_bytes,
+                          Launch launch) {
+  AttnPlan pl;
+  const exl3_status st = plan_attention(p.batch, p.tokens, q_heads, p.heads_kv, head_dim, &pl);
+  return st != EXL3_OK ? st : run_planned(p, pl, workspace, workspace_bytes, launch);
 }
 
 }  // namespace exl3

@@ -161,6 +161,7 @@ struct Work {
   int kv_len;
   int part;           // splits > 1: the part's number among those of all split tiles
   int first;          // ATTN_OWN: the first key
+  int item;           // ATTN_PREFIX: the item's number
 };
 
 // Every wave of the workgroup finds the same answer.  Sequence s has
@@ -254,6 +255,10 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       w.q_len = __builtin_amdgcn_readlane(x.ql, l);
       w.kv_len = __builtin_amdgcn_readlane(x.kv, l);
       if constexpr (KIND == ATTN_OWN) w.first = __builtin_amdgcn_readlane(x.first, l);
+      if constexpr (KIND == ATTN_PREFIX) {
+        w.item = item;
+        return item < p.part_cap;
+      }
       w.part = w.splits > 1 ? pbase + __builtin_amdgcn_readlane(pincl - parts, l) + at : 0;
       // (lengths that are written while the call runs could make more parts than there is room for)
       return w.splits == 1 || w.part - w.split + w.splits <= p.part_cap;
@@ -321,10 +326,46 @@ __device__ __forceinline__ KeyRange sink_range(const AttnParams &p, const Work &
   return k;
 }
 
-// The state of row r of the tile's sequence.
-__device__ __forceinline__ float *state_row(const AttnParams &p, const Work &w, int r, int head, int D) {
-  const int i = quotient(r, p.by_group), h = r - i * p.group;
-  return p.state + ((int64_t)(w.q0 + i) * (p.heads_kv * p.group) + head * p.group + h) * (STATE_PAD + D);
+// ------------------------------------------- shared keys, then own keys
+//
+// Every part of a group's tile leaves its rows (maximum, sum, result; nothing
+// is joined there), and each of the group's rows adds up its parts, in their
+// order, when its own keys are done.  Joined by the last part to arrive, as
+// split tiles are below, 64 sequences over 24000 shared keys, 128 rows a tile in
+// 24 parts of 66 KB, took 72 us for the shared keys;
+// now 46 (in 32 parts of 768), and the own keys 8 more.
+
+// Row r of an item's tile of 2^shift rows.
+template <int D>
+__device__ __forceinline__ float *state_row(const AttnParams &p, int item, int head, int shift, int r) {
+  return p.state + (((int64_t)item * p.heads_kv + head) * (1 << shift) + r) * (STATE_PAD + D);
+}
+
+// ATTN_PREFIX: where the group's items start, for ATTN_OWN.
+__device__ __forceinline__ void note_items(const AttnParams &p, const Work &w, int head) {
+  if (threadIdx.x == 0 && head == 0 && w.tile == 0 && w.split == 0) {
+    p.group_items[2 * w.seq] = w.item;
+    p.group_items[2 * w.seq + 1] = w.splits;
+  }
+}
+
+// ATTN_OWN: the rows that the group's parts left for row r of the sequence's
+// rows: `parts` of them, `step` floats apart.
+struct Left {
+  const float *row;
+  int64_t step;
+  int parts;
+};
+template <int D>
+__device__ __forceinline__ Left left_for(const AttnParams &p, const Work &w, int r, int head) {
+  const int g = p.group_of[w.seq];
+  const int at = r + (w.q0 - p.group_row[g]) * p.group;  // of the group's rows on this head
+  const int first = p.group_items[2 * g], parts = p.group_items[2 * g + 1];
+  Left x;
+  x.row = state_row<D>(p, first + (at >> p.state_shift) * parts, head, p.state_shift, at & ((1 << p.state_shift) - 1));
+  x.step = (int64_t)p.heads_kv * ((STATE_PAD + D) << p.state_shift);
+  x.parts = parts;
+  return x;
 }
 
 // ------------------------------------------------- parts of a split tile

@@ -103,7 +103,14 @@ struct AttnParams {
   int32_t sinks, sink_keys;   // ATTN_SINKS: first keys that stay visible, and that rounded up to whole tiles
   const int32_t *table_row;   // ATTN_PREFIX: the row of the page table for each sequence (a group of them)
   const int32_t *start;       // ATTN_OWN: the first key of each sequence, those before being in the state
-  float *state;               // ATTN_PREFIX writes, ATTN_OWN reads: [tokens][q heads] rows of STATE_PAD + D floats
+  // What ATTN_PREFIX leaves for ATTN_OWN: for every work item and key/value
+  // head the rows of its tile, STATE_PAD + D floats each, and where a group's
+  // items are.
+  float *state;
+  int32_t *group_items;        // [groups][2]: the first item, and the parts of each tile
+  const int32_t *group_of;     // ATTN_OWN: [batch] the group of each sequence
+  const int32_t *group_row;    // and [groups] the first row of each
+  int32_t state_shift;         // log2 of a tile's rows there
 };
 constexpr int STATE_PAD = 4;  // maximum and sum of a row before its D sums, which stay 16-byte aligned
 

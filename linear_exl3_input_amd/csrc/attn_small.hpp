@@ -157,8 +157,11 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   constexpr int DP = D / 32;             // as pairs
   using KR = KeyRun<D, CB>;
   constexpr int VW = DV * CB >= 32 ? DV * CB / 32 : 1;  // words of a lane's dims of one value row
-  __shared__ float s_o[4][4][64][DV + 1];  // [element i][wave][lane][operand j]
+  __shared__ __align__(16) float s_o[4][4][64][DV + 1];  // [element i][wave][lane][operand j]
   __shared__ float s_m[4][R], s_l[4][R];
+  constexpr bool OWN = KIND == ATTN_OWN;
+  __shared__ float4_t s_left[OWN ? R : 1][OWN ? D / 4 : 1], s_sums[OWN ? 256 : 1];  // of the shared keys
+  __shared__ float2_t s_left_ml[OWN ? R : 1], s_sums_ml[OWN ? 256 : 1];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
@@ -298,6 +301,81 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   if (k0 < end) {
     load_k(k0, pk);
     load_v(k0, pv);
+  }
+  // What the shared keys' parts left for the tile's rows, to LDS: a thread has 4
+  // dims of a row and all parts, or, of many, every fourth, whose sums then meet.
+  // With whole sequences this is done here, while the first keys are on their
+  // way.  64 sequences of up to 1500 own keys, 8 heads of 128, 32 parts: 39 us
+  // with the 34 MB that these left, 31 with one part (a lane of the rows alone,
+  // after the last key: 49).
+  auto collect = [&]() __attribute__((always_inline)) {
+    constexpr int Q = D / 4;  // threads of a row
+    constexpr int U = 8;      // parts in flight (16: no faster)
+    const int n_rows = r_last - r0 + 1;
+    const Left all = left_for<D>(p, w, r0, head);
+    // loads one after another: either way, a row's parts by one thread or by four
+    constexpr int ROWS = 256 / Q;
+    const int alone = (n_rows + ROWS - 1) / ROWS * ((all.parts + U - 1) / U);
+    const int by_four = (n_rows + ROWS / 4 - 1) / (ROWS / 4) * ((all.parts + 4 * U - 1) / (4 * U));
+    const int s_log2 = by_four < alone ? 2 : 0;
+    const int q = threadIdx.x % Q, at = threadIdx.x / Q;
+    const int part = at & ((1 << s_log2) - 1), rp = at >> s_log2, RP = 256 / Q >> s_log2;
+    for (int first_row = 0; first_row < n_rows; first_row += RP) {
+      const Left left = left_for<D>(p, w, r0 + min(first_row + rp, n_rows - 1), head);
+      float mx = -INFINITY, lx = 0.f;
+      float4_t ox = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int x = part; x < left.parts; x += U << s_log2) {
+        float2_t ml[U];
+        float4_t v[U];
+#pragma unroll
+        for (int y = 0; y < U; ++y) {
+          const float *row = left.row + min(x + (y << s_log2), left.parts - 1) * left.step;
+          ml[y] = *(const float2_t *)row;
+          v[y] = *(const float4_t *)(row + STATE_PAD + 4 * q);
+        }
+        float grown = mx;
+#pragma unroll
+        for (int y = 0; y < U; ++y) grown = __builtin_fmaxf(grown, ml[y].x);
+        const float base = grown == -INFINITY ? 0.f : grown;
+        const float keep = __builtin_amdgcn_exp2f(mx - base);
+        mx = grown;
+        lx *= keep;
+        ox *= keep;
+#pragma unroll
+        for (int y = 0; y < U; ++y)
+          if (x + (y << s_log2) < left.parts) {
+            const float f = __builtin_amdgcn_exp2f(ml[y].x - base);
+            lx += ml[y].y * f;
+            ox += v[y] * f;
+          }
+      }
+      if (s_log2 > 0) {  // the same for all threads
+        __syncthreads();  // the sums of the rows before have been read
+        s_sums[threadIdx.x] = ox;
+        s_sums_ml[threadIdx.x] = (float2_t){mx, lx};
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+          for (int y = 1; y < 4; ++y) {
+            const float2_t ml = s_sums_ml[threadIdx.x + y * Q];
+            const float grown = __builtin_fmaxf(mx, ml.x), base = grown == -INFINITY ? 0.f : grown;
+            const float keep = __builtin_amdgcn_exp2f(mx - base), f = __builtin_amdgcn_exp2f(ml.x - base);
+            mx = grown;
+            lx = lx * keep + ml.y * f;
+            ox = ox * keep + s_sums[threadIdx.x + y * Q] * f;
+          }
+        }
+      }
+      if (part == 0 && first_row + rp < n_rows) {
+        s_left[first_row + rp][q] = ox;
+        if (q == 0) s_left_ml[first_row + rp] = (float2_t){mx, lx};
+      }
+    }
+    __syncthreads();
+  };
+  if constexpr (OWN) {
+    if (w.first > 0 && w.splits == 1) collect();
   }
   bool odd = false;  // some value that not all rows see is an infinity or NaN
   for (; k0 < end; k0 += 128) {
@@ -501,6 +579,20 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     for (int j = 0; j < DV; ++j)
       mine[n][j] = (s_o[wave][0][lane][j] + s_o[wave][1][lane][j]) + (s_o[wave][2][lane][j] + s_o[wave][3][lane][j]);
   }
+  if constexpr (KIND == ATTN_PREFIX) {
+    note_items(p, w, head);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (!live[n]) continue;
+      float *y = state_row<D>(p, w.item, head, NT == 2 ? 5 : 4, 16 * n + c);
+      if (wave == 0 && g == 0) *(float2_t *)y = (float2_t){top[n], total[n]};
+#pragma unroll
+      for (int j = 0; j < DV; j += 4)
+        *(float4_t *)(y + STATE_PAD + DV * (4 * g + wave) + j) =
+            (float4_t){mine[n][j], mine[n][j + 1], mine[n][j + 2], mine[n][j + 3]};
+    }
+    return;
+  }
   if (w.splits > 1) {
     // a part: o as [n][wave][lane][DV], then m and the sum of each row; rows
     // that the tile does not have are neither written nor read
@@ -572,31 +664,23 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     put(w.split);
     if (!add_parts(p, w, head, add, put)) return;
   }
-  if constexpr (KIND == ATTN_PREFIX || KIND == ATTN_OWN) {
-    const int d = DV * (4 * g + wave);
+  if constexpr (KIND == ATTN_OWN) {
+    if (w.first > 0) {
+      if (w.splits > 1) collect();
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (!live[n] || (KIND == ATTN_OWN && w.first <= 0)) continue;
-      float *y = state_row(p, w, r0 + 16 * n + c, head, D);
-      if constexpr (KIND == ATTN_PREFIX) {
-        if (wave == 0 && g == 0) *(float2_t *)y = (float2_t){top[n], total[n]};
-#pragma unroll
-        for (int j = 0; j < DV; j += 4)
-          *(float4_t *)(y + STATE_PAD + d + j) = (float4_t){mine[n][j], mine[n][j + 1], mine[n][j + 2], mine[n][j + 3]};
-      } else {
-        const float2_t ml = *(const float2_t *)y;
+      for (int n = 0; n < NT; ++n) {
+        const float2_t ml = s_left_ml[16 * n + c];
         const float grown = __builtin_fmaxf(top[n], ml.x), base = grown == -INFINITY ? 0.f : grown;
-        const float keep = __builtin_amdgcn_exp2f(top[n] - base), more = __builtin_amdgcn_exp2f(ml.x - base);
-        total[n] = total[n] * keep + ml.y * more;
+        const float keep = __builtin_amdgcn_exp2f(top[n] - base), f = __builtin_amdgcn_exp2f(ml.x - base);
+        total[n] = total[n] * keep + ml.y * f;
 #pragma unroll
         for (int j = 0; j < DV; j += 4) {
-          const float4_t x = *(const float4_t *)(y + STATE_PAD + d + j);
+          const float4_t v = s_left[16 * n + c][(DV * (4 * g + wave) + j) / 4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mine[n][j + i] = mine[n][j + i] * keep + x[i] * more;
+          for (int i = 0; i < 4; ++i) mine[n][j + i] = mine[n][j + i] * keep + v[i] * f;
         }
       }
     }
-    if constexpr (KIND == ATTN_PREFIX) return;
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n)

@@ -94,24 +94,68 @@ exl3_status run_sinks(AttnParams &p, int32_t head_dim, bool bf16, int32_t bits, 
                        [&](int columns) { return launch_attn_sinks(head_dim, bf16, bits, p, columns, s); });
 }
 
-// The workspace of a call with shared prefixes: the counters, the parts of
-// either pass, what the groups are, and the state of every row.
+// The workspace of a call with shared prefixes: the counters and the own keys'
+// parts, what the groups are, and the state of every part's rows.
 struct PrefixPlan {
   AttnPlan shared, own;  // the groups as sequences; the sequences
+  int32_t items;         // of the shared keys, at most, on each key/value head
+  int32_t rows_log2;     // rows of an item
   size_t ints, state, workspace;  // offsets
 };
+
+// A call whose shared keys, read by every sequence for itself, are fewer bytes
+// than this is paged_attention's: they come from the caches at 8 to 9 TB/s, and
+// the two passes and the groups take 20 us before the first key.  Measured
+// shared / plain, one token, 32/8 heads of 128, 8 bits: 4 sequences of 8192 and
+// 32768 shared keys (54 and 210 MB) 24 / 21 us and 34 / 42, 8 (126, 489) 27 / 25
+// and 39 / 67, 16 (75, 270) 24 / 27 and 28 / 46, 64 of 512 and 2048 (111, 315) 31
+// / 27 and 34 / 48; 8 tokens each, 16 of 8192 (270) 54 / 51; 16 of 16384, 24/4
+// heads of 256, 4 bits (273) 56 / 50.  The host knows the page table's width
+// alone, so that counts as every sequence's keys.
+constexpr double SHARED_BYTES_MIN = 192e6;
+
+bool worth_sharing(const exl3_kv_cache *c, int32_t page_table_width, int32_t batch, int32_t groups) {
+  const double row = c->head_dim * c->bits / 8.0 + (c->bits < 16 ? c->head_dim / 32.0 : 0.0);
+  return (double)(batch - groups) * page_table_width * c->page_size * c->heads * 2 * row >= SHARED_BYTES_MIN;
+}
 
 exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q_heads, int32_t kv_heads,
                         int32_t head_dim, PrefixPlan *pl) {
   exl3_status st;
   if (groups < 0 || groups > batch)
     return host_fail(EXL3_ERR_INVALID_ARG, "groups=%d, must be 0..batch=%d", groups, batch);
-  if ((st = plan_attention(batch, tokens, q_heads, kv_heads, head_dim, &pl->own)) != EXL3_OK) return st;
-  if ((st = plan_attention(groups, tokens, q_heads, kv_heads, head_dim, &pl->shared)) != EXL3_OK) return st;
+  // Own keys: 16 rows a workgroup rather than 32, since each of them reads what
+  // the shared keys left for its rows (16 sequences of 8 tokens, 8 heads of 128:
+  // 19 us, with 32 rows 29), and in parts only where whole sequences do not
+  // fill the GPU (64 sequences of up to 1500 own keys: 39 us whole, 44 in parts).
+  const int32_t own = plan_columns(batch, tokens, q_heads, kv_heads, head_dim);
+  st = plan_split(batch, tokens, q_heads, kv_heads, head_dim, std::min(own, 1), &pl->own);
+  if (st != EXL3_OK) return st;
+  if ((int64_t)batch * kv_heads >= host_cus()) {
+    pl->own.target = pl->own.part_cap = 0;
+    pl->own.workspace = 0;
+  }
+  pl->own.part_min = std::max(pl->own.part_min, 1024);
+  // Shared keys: as many parts as fill the GPU once, since joining them is cheap
+  // (state_row): two workgroups of the tile kernel a CU (one with heads of
+  // 256), one of the small kernel.
+  pl->shared.columns = plan_columns(groups, tokens, q_heads, kv_heads, head_dim);
+  const bool tile = pl->shared.columns == 0;
+  pl->shared.target = std::max(1, (tile && head_dim < 256 ? 2 : 1) * host_cus() / kv_heads);
+  pl->shared.part_min = 256;
+  pl->rows_log2 = __builtin_ctz((unsigned)tile_rows(pl->shared.columns));
+  const int64_t items = ((int64_t)tokens * (q_heads / kv_heads) >> pl->rows_log2) + groups + pl->shared.target;
+  if (items * kv_heads > MAX_GRID)
+    return host_fail(EXL3_ERR_UNSUPPORTED, "%d tokens x %d heads: more tiles than a launch holds", tokens, q_heads);
+  pl->items = (int32_t)items;
   auto whole = [](size_t n) { return (n + 255) & ~(size_t)255; };
-  pl->ints = whole(std::max({pl->own.workspace, pl->shared.workspace, (size_t)EXL3_WORKSPACE_COUNTER_BYTES}));
-  pl->state = pl->ints + whole(sizeof(int32_t) * (2 * (size_t)batch + 1 + 3 * (size_t)groups + 2));
-  pl->workspace = pl->state + sizeof(float) * (size_t)tokens * q_heads * (STATE_PAD + head_dim);
+  pl->ints = whole(std::max(pl->own.workspace, (size_t)EXL3_WORKSPACE_COUNTER_BYTES));
+  pl->state = pl->ints + whole(sizeof(int32_t) * (3 * (size_t)batch + 1 + 5 * (size_t)groups + 2));
+  AttnPlan plain;  // a call that is not worth it
+  if ((st = plan_attention(batch, tokens, q_heads, kv_heads, head_dim, &plain)) != EXL3_OK) return st;
+  pl->workspace =
+      pl->state + sizeof(float) * ((size_t)pl->items * kv_heads << pl->rows_log2) * (STATE_PAD + head_dim);
+  pl->workspace = std::max(pl->workspace, plain.workspace);
   return EXL3_OK;
 }
 
@@ -334,13 +378,35 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
     return host_fail(EXL3_ERR_WORKSPACE, "workspace of %zu bytes; this call needs %zu (short by %zu)", workspace_bytes,
                      pl.workspace, pl.workspace > workspace_bytes ? pl.workspace - workspace_bytes : (size_t)0);
   if ((st = check_ptr(workspace, "workspace")) != EXL3_OK) return st;
+  if (!worth_sharing(c, page_table_width, batch, groups))
+    return exl3_paged_attention(c, q, out, cu_q, kv_len, page_table, page_table_stride, page_table_width, batch, tokens,
+                                scale, 0, workspace, workspace_bytes, stream);
   const hipStream_t s = (hipStream_t)stream;
   const bool bf16 = c->dtype == EXL3_BF16;
   char *ws = static_cast<char *>(workspace);
   int32_t *ints = reinterpret_cast<int32_t *>(ws + pl.ints);
-  const GroupsParams g = {cu_q,       kv_len, group_cu,     prefix_len,       batch,
-                          tokens,     groups, p.table_keys, ints,             ints + batch + 1,
-                          ints + 2 * batch + 1, ints + 2 * batch + 1 + groups + 1, ints + 2 * batch + 1 + 2 * (groups + 1)};
+  auto take = [&](int64_t n) {
+    int32_t *at = ints;
+    ints += n;
+    return at;
+  };
+  GroupsParams g;
+  std::memset(&g, 0, sizeof g);
+  g.cu = cu_q;
+  g.kv_len = kv_len;
+  g.group_cu = group_cu;
+  g.prefix_len = prefix_len;
+  g.batch = batch;
+  g.tokens = tokens;
+  g.groups = groups;
+  g.table_keys = p.table_keys;
+  g.seq_row = take(batch + 1);
+  g.start = take(batch);
+  g.of = take(batch);
+  g.first = take(groups + 1);
+  g.row = take(groups + 1);
+  g.keys = take(groups);
+  p.group_items = take(2 * (int64_t)groups);
   if ((st = launched(launch_groups(g, s), "groups launch")) != EXL3_OK) return st;
   p.state = reinterpret_cast<float *>(ws + pl.state);
   if (groups > 0) {
@@ -350,13 +416,18 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
     shared.table_row = g.first;
     shared.batch = groups;
     shared.causal = 0;
-    st = run_attention(shared, D, q->heads, workspace, workspace_bytes,
-                       [&](int columns) { return launch_attn_prefix(D, bf16, c->bits, shared, columns, s); });
+    shared.target = pl.shared.target;
+    shared.part_min = pl.shared.part_min;
+    shared.part_cap = pl.items;
+    st = launched(launch_attn_prefix(D, bf16, c->bits, shared, pl.shared.columns, s), "shared keys launch");
     if (st != EXL3_OK) return st;
   }
   p.start = g.start;
-  return run_attention(p, D, q->heads, workspace, workspace_bytes,
-                       [&](int columns) { return launch_attn_own(D, bf16, c->bits, p, columns, s); });
+  p.group_of = g.of;
+  p.group_row = g.row;
+  p.state_shift = pl.rows_log2;
+  return run_planned(p, pl.own, workspace, workspace_bytes,
+                     [&](int columns) { return launch_attn_own(D, bf16, c->bits, p, columns, s); });
 }
 
 }  // extern "C"

@@ -31,6 +31,7 @@ struct GroupsParams {
   int32_t *first;                        // [groups+1] the first sequence of each group
   int32_t *row;                          // [groups+1] the first row of each group
   int32_t *keys;                         // [groups] its shared keys
+  int32_t *of;                           // [batch] the group of each sequence that shares keys
 };
 
 hipError_t launch_groups(const GroupsParams &p, hipStream_t s);

@@ -16,6 +16,15 @@ BF16, F16 = torch.bfloat16, torch.float16
 same_bits, normal = base.same_bits, base.normal
 
 
+def widened(cache, table):
+    """The page table as a part of one with so many columns that a call for two sequences and one group shares."""
+    row = cache.head_dim * cache.bits // 8 + (cache.head_dim // 32 if cache.bits < 16 else 0)
+    columns = int(200e6 / (cache.page_size * cache.heads * 2 * row)) + 1
+    big = torch.full((table.shape[0], max(columns, table.shape[1])), -1, dtype=torch.int32, device="cuda")
+    big[:, :table.shape[1]] = table
+    return big
+
+
 class Shared:
     """Groups of sequences: groups[g] = (prefix keys, [(new tokens, keys after the prefix), ...]).  Shared keys lie in the
     same pages, whole ones; the rest of them begins every sequence's own pages.  A key count below zero shortens the
@@ -64,14 +73,17 @@ class Shared:
                 slots = self.table[s, pos(n) // self.page].long() * self.page + pos(n) % self.page
                 ex.cache_write(self.cache, self.front[g][0].cuda(), self.front[g][1].cuda(), slots.int().cuda())
 
-    def args(self):
-        return (self.cache, self.q.cuda(), self.cu.cuda(), torch.tensor(self.kv_lens, dtype=torch.int32).cuda(), self.table.cuda())
+    def args(self, wide=True):
+        """Arguments with a page table of wide rows, by whose size the call goes for the shared passes, or as it is."""
+        table = self.table.cuda()
+        return (self.cache, self.q.cuda(), self.cu.cuda(), torch.tensor(self.kv_lens, dtype=torch.int32).cuda(),
+                widened(self.cache, table) if wide else table)
 
     def run(self, group_cu=None, prefix=None, **kw):
         ints = lambda x, y: (x if y is None else torch.tensor(y, dtype=torch.int32)).cuda()  # noqa: E731
         # what is shared in earnest: whole pages
         shared = torch.tensor(self.shared, dtype=torch.int32)
-        return ex.prefix_attention(*self.args(), ints(self.group_cu, group_cu), ints(shared, prefix), **kw)
+        return ex.prefix_attention(*self.args(kw.pop("wide", True)), ints(self.group_cu, group_cu), ints(shared, prefix), **kw)
 
     def expect(self, scale=None):
         bits, d = self.cache.bits, self.q.shape[-1]
@@ -87,6 +99,8 @@ class Shared:
     def check(self, what="", **kw):
         want = self.expect()
         ref.check(self.run(**kw), *want, what or "attention")
+        # and the call that its sizes leave to the plain kernels
+        ref.check(self.run(wide=False, **kw), *want, "narrow")
         return want
 
 
@@ -167,6 +181,7 @@ def test_holes():
     assert not x.run()[6:].any()
     kv, cu = torch.tensor(x.kv_lens, dtype=torch.int32).cuda(), x.cu.cuda()
     x.table[:, 3:] = -1  # a table narrower than the prefix
+    ref.check(x.run(), *x.expect(), "shared pages after the third gone")
     got = ex.prefix_attention(x.cache, x.q.cuda(), cu, kv, x.table[:, :3].contiguous().cuda(), x.group_cu.cuda(), x.prefix.cuda())
     ref.check(got, *x.expect(), "narrow")
     none = torch.zeros(5, 0, dtype=torch.int32, device="cuda")
@@ -222,6 +237,8 @@ def test_lengths_that_do_not_fit_stay_inside_the_buffers():
     assert not got[4:8].any() and (got.double() - plain.double()).abs().max() <= 4 * 2.0 ** -8 * plain.double().abs().max()
     cu2 = torch.tensor([0, 4, 2, 9000], dtype=torch.int32).cuda()
     got = ex.prefix_attention(cache, q, cu2, kv, table, groups, shared)
+    plain = ex.paged_attention(cache, q, cu2, kv, table)
+    assert (got[:2].double() - plain[:2].double()).abs().max() <= 4 * 2.0 ** -8 * plain[:2].double().abs().max()
     assert (got[:4].double() - want[:4].double()).abs().max() <= 4 * 2.0 ** -8 * want.double().abs().max()
 
 
@@ -289,6 +306,7 @@ def test_cache_past_four_gigabytes():
     pos = torch.arange(300, dtype=torch.int32, device="cuda")
     for s in range(3):
         ex.cache_write(cache, k[s].cuda(), v[s].cuda(), cache.slots(table, torch.full_like(pos, s), pos))
+    table = widened(cache, table)
     for n in (1, 60):
         q = normal(g, (3 * n, 8, 64), BF16)
         ints = lambda *x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
