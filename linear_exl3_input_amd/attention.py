@@ -695,11 +695,13 @@ def cache_extend(cache: KvCache, q_len: torch.Tensor, kv_len: torch.Tensor, page
     at = [_ints(q_len, "q_len", B, dev), _ints(kv_len, "kv_len", B, dev)]
     free_at = _ints(free_pages, "free_pages", free_pages.shape[0], dev)
     taken_at = None if taken is None else _ints(taken, "taken", 1, dev)
+    sizes = (B + 1, B, tokens, tokens, 2)
     if out is None:
-        # views of one new tensor
-        out = CacheStep(*kv_len.new_empty(2 * B + 1 + 2 * tokens + 2).split((B + 1, B, tokens, tokens, 2)))
-    made = [_ints(t, f"out.{name}", n, dev) for t, name, n in
-            zip(out, CacheStep._fields, (B + 1, B, tokens, tokens, 2))]
+        new = kv_len.new_empty(2 * B + 3 + 2 * tokens)  # all of them are views of it
+        out, a = CacheStep(*new.split(sizes)), new.data_ptr()
+        made = (a, a + 4 * (B + 1), a + 4 * (2 * B + 1), a + 4 * (2 * B + 1 + tokens), a + 4 * (2 * B + 1 + 2 * tokens))
+    else:
+        made = [_ints(t, name, n, dev) for t, name, n in zip(out, CacheStep._fields, sizes)]
     _check(_lib().exl3_cache_extend(cache.pages, cache.page_size, *at, B, page_table.data_ptr(), page_table.stride(0),
                                     page_table.shape[1], free_at, free_pages.shape[0], taken_at, tokens, *made,
                                     _raw_stream(dev.index)))

@@ -237,9 +237,9 @@ inline int32_t plan_columns(int32_t batch, int32_t tokens, int32_t q_heads, int3
   return rows > tile_min_rows(batch, kv_heads, head_dim) ? 0 : rows > 16.0 && head_dim < 256 ? 2 : 1;
 }
 
-// The split of a call's keys with a kernel, from its sizes alone.
+// The split of a call's keys with a kernel, from its sizes alone (or for so many rounds).
 inline exl3_status plan_split(int32_t batch, int32_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                              int32_t columns, AttnPlan *pl) {
+                              int32_t columns, AttnPlan *pl, int32_t for_rounds = 0) {
   const int32_t group = q_heads / kv_heads;
   pl->columns = columns;
   pl->target = 0;
@@ -250,7 +250,7 @@ inline exl3_status plan_split(int32_t batch, int32_t tokens, int32_t q_heads, in
   const int64_t tiles = (int64_t)tokens * group / R + batch;  // at most, on each key/value head
   const int64_t per_cu = (tile ? head_dim == 256 : head_dim * pl->columns >= 256) ? 1 : 2;  // workgroups of a round
   const int64_t round = per_cu * host_cus();
-  const int64_t rounds = 4 * tiles * kv_heads <= round ? 1 : tile ? 4 : 2;
+  const int64_t rounds = for_rounds > 0 ? for_rounds : 4 * tiles * kv_heads <= round ? 1 : tile ? 4 : 2;
   const int64_t want = std::max<int64_t>(kv_heads, rounds * round);
   pl->part_cap = 0;
   const int64_t parts = std::min(2 * (want / kv_heads), want / kv_heads + tiles);
