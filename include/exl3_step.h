@@ -66,7 +66,7 @@ exl3_status exl3_norm_rope_cache_write(const exl3_kv_cache *c, const exl3_rotary
  * taken: NULL (0) or one int32, the free pages used by earlier steps.  A row
  * whose page is not one of the cache's has slot -1.  q_len counts as 0..2^20,
  * kv_len as 0..2^30, taken as 0..n_free.  Outputs overlap neither inputs nor
- * each other; page_table is in both. */
+ * each other; page_table (from its first row to the end of its last) is both. */
 exl3_status exl3_cache_extend(int32_t pages, int32_t page_size, const int32_t *q_len, const int32_t *kv_len,
                               int32_t batch, int32_t *page_table, int64_t page_table_stride, int32_t page_table_width,
                               const int32_t *free_pages, int32_t n_free, const int32_t *taken, int32_t tokens,
