@@ -304,7 +304,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   }
   // What the shared keys' parts left for the tile's rows, to LDS: a thread has 4
   // dims of a row and all parts, or, of many, every fourth, whose sums then meet.
-  // With whole sequences this is done here, while the first keys are on their
+  // The first part of the own keys does it, while its first keys are on their
   // way.  64 sequences of up to 1500 own keys, 8 heads of 128, 32 parts: 39 us
   // with the 34 MB that these left, 31 with one part (a lane of the rows alone,
   // after the last key: 49).
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     __syncthreads();
   };
   if constexpr (OWN) {
-    if (w.first > 0 && w.splits == 1) collect();
+    if (w.first > 0 && w.split == 0) collect();
   }
   bool odd = false;  // some value that not all rows see is an infinity or NaN
   for (; k0 < end; k0 += 128) {
@@ -593,6 +593,24 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     }
     return;
   }
+  if constexpr (KIND == ATTN_OWN) {
+    if (w.first > 0 && w.split == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float2_t ml = s_left_ml[16 * n + c];
+        const float grown = __builtin_fmaxf(top[n], ml.x), base = grown == -INFINITY ? 0.f : grown;
+        const float keep = __builtin_amdgcn_exp2f(top[n] - base), f = __builtin_amdgcn_exp2f(ml.x - base);
+        top[n] = grown;
+        total[n] = total[n] * keep + ml.y * f;
+#pragma unroll
+        for (int j = 0; j < DV; j += 4) {
+          const float4_t v = s_left[16 * n + c][(DV * (4 * g + wave) + j) / 4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mine[n][j + i] = mine[n][j + i] * keep + v[i] * f;
+        }
+      }
+    }
+  }
   if (w.splits > 1) {
     // a part: o as [n][wave][lane][DV], then m and the sum of each row; rows
     // that the tile does not have are neither written nor read
@@ -663,24 +681,6 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     };
     put(w.split);
     if (!add_parts(p, w, head, add, put)) return;
-  }
-  if constexpr (KIND == ATTN_OWN) {
-    if (w.first > 0) {
-      if (w.splits > 1) collect();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float2_t ml = s_left_ml[16 * n + c];
-        const float grown = __builtin_fmaxf(top[n], ml.x), base = grown == -INFINITY ? 0.f : grown;
-        const float keep = __builtin_amdgcn_exp2f(top[n] - base), f = __builtin_amdgcn_exp2f(ml.x - base);
-        total[n] = total[n] * keep + ml.y * f;
-#pragma unroll
-        for (int j = 0; j < DV; j += 4) {
-          const float4_t v = s_left[16 * n + c][(DV * (4 * g + wave) + j) / 4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mine[n][j + i] = mine[n][j + i] * keep + v[i] * f;
-        }
-      }
-    }
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n)

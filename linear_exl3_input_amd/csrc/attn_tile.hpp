@@ -615,6 +615,33 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     }
     return;
   }
+  if constexpr (KIND == ATTN_OWN) {
+    if (w.first > 0 && w.split == 0 && row < rows) {
+      const Left left = left_for<D>(p, w, row, head);
+      const float before = m;
+#pragma unroll 4
+      for (int x = 0; x < left.parts; ++x) m = __builtin_fmaxf(m, left.row[x * left.step]);
+      const float base = m == -INFINITY ? 0.f : m, keep = __builtin_amdgcn_exp2f(before - base);
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= keep;
+#pragma unroll 1
+      for (int x = 0; x < left.parts; ++x) {
+        const float *from = left.row + x * left.step;
+        const float2_t ml = *(const float2_t *)from;
+        const float f = __builtin_amdgcn_exp2f(ml.x - base);
+        l += ml.y * f;
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const float4_t v = *(const float4_t *)(from + STATE_PAD + 8 * piece_of(y, h) + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[prod(j + i)][elem(y, j + i)] += v[i] * f;
+          }
+      }
+    }
+  }
   if (w.splits > 1) {
     // a part: [wave][o register / 4][lane][4], then m and the sum of each row;
     // waves whose rows the tile does not have neither write nor read
@@ -673,33 +700,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
     };
     put(w.split);
     if (!add_parts(p, w, head, add, put)) return;
-  }
-  if constexpr (KIND == ATTN_OWN) {
-    if (w.first > 0 && row < rows) {
-      const Left left = left_for<D>(p, w, row, head);
-      const float before = m;
-#pragma unroll 4
-      for (int x = 0; x < left.parts; ++x) m = __builtin_fmaxf(m, left.row[x * left.step]);
-      const float base = m == -INFINITY ? 0.f : m, keep = __builtin_amdgcn_exp2f(before - base);
-      l *= keep;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] *= keep;
-#pragma unroll 1
-      for (int x = 0; x < left.parts; ++x) {
-        const float *from = left.row + x * left.step;
-        const float2_t ml = *(const float2_t *)from;
-        const float f = __builtin_amdgcn_exp2f(ml.x - base);
-        l += ml.y * f;
-#pragma unroll
-        for (int y = 0; y < D / 16; ++y)
-#pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const float4_t v = *(const float4_t *)(from + STATE_PAD + 8 * piece_of(y, h) + j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[prod(j + i)][elem(y, j + i)] += v[i] * f;
-          }
-      }
-    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key is zero
   int ln = lane;
