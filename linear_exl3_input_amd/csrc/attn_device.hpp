@@ -328,12 +328,18 @@ __device__ __forceinline__ KeyRange sink_range(const AttnParams &p, const Work &
 
 // ------------------------------------------- shared keys, then own keys
 //
-// Every part of a group's tile leaves its rows (maximum, sum, result; nothing
-// is joined there), and each of the group's rows adds up its parts, in their
-// order, when its own keys are done.  Joined by the last part to arrive, as
-// split tiles are below, 64 sequences over 24000 shared keys, 128 rows a tile in
-// 24 parts of 66 KB, took 72 us for the shared keys;
-// now 46 (in 32 parts of 768), and the own keys 8 more.
+// With o1, l1 the sums of a row over the shared keys under their maximum m1, and
+// o2, l2, m2 those over its own: m = max(m1, m2) and
+//   o = (o1 2^(m1-m) + o2 2^(m2-m)) / (l1 2^(m1-m) + l2 2^(m2-m)).
+// Every part of a group's tile leaves its rows (m, l, o; nothing is joined
+// there), and the first part of a row's own keys adds them up in a fixed order.
+// What bounds the shared keys is vector work beside the products at 8 bits (matrix
+// units busy 20% of the cycles, vector units 37%) and a start and end of 11 us;
+// the own keys the latency of the longest sequence.  Measured: 64 sequences
+// over 24000 shared and up to 1500 own keys, 32/8 heads of 128, 8 bits: 46 us
+// for the shared keys in 32 parts of 768, 39 for the own, of which 8 are the 34 MB
+// that the parts left.  (Joined by the last part to arrive, as split tiles are
+// below, 24 parts of 66 KB: 72 and 31 us.)
 
 // Row r of an item's tile of 2^shift rows.
 template <int D>
@@ -350,7 +356,8 @@ __device__ __forceinline__ void note_items(const AttnParams &p, const Work &w, i
 }
 
 // ATTN_OWN: the rows that the group's parts left for row r of the sequence's
-// rows: `parts` of them, `step` floats apart.
+// rows: `parts` of them, `step` floats apart.  (Within the state whatever
+// offsets are written while the call runs.)
 struct Left {
   const float *row;
   int64_t step;
@@ -360,9 +367,10 @@ template <int D>
 __device__ __forceinline__ Left left_for(const AttnParams &p, const Work &w, int r, int head) {
   const int g = p.group_of[w.seq];
   const int at = r + (w.q0 - p.group_row[g]) * p.group;  // of the group's rows on this head
-  const int first = p.group_items[2 * g], parts = p.group_items[2 * g + 1];
+  const int parts = min(max(p.group_items[2 * g + 1], 0), p.state_items);
+  const int first = min(max(p.group_items[2 * g] + (at >> p.state_shift) * parts, 0), p.state_items - parts);
   Left x;
-  x.row = state_row<D>(p, first + (at >> p.state_shift) * parts, head, p.state_shift, at & ((1 << p.state_shift) - 1));
+  x.row = state_row<D>(p, first, head, p.state_shift, at & ((1 << p.state_shift) - 1));
   x.step = (int64_t)p.heads_kv * ((STATE_PAD + D) << p.state_shift);
   x.parts = parts;
   return x;

@@ -111,6 +111,7 @@ struct AttnParams {
   const int32_t *group_of;     // ATTN_OWN: [batch] the group of each sequence
   const int32_t *group_row;    // and [groups] the first row of each
   int32_t state_shift;         // log2 of a tile's rows there
+  int32_t state_items;         // and the items that the state holds
 };
 constexpr int STATE_PAD = 4;  // maximum and sum of a row before its D sums, which stay 16-byte aligned
 

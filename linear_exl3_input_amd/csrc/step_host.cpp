@@ -438,6 +438,7 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
   p.group_of = g.of;
   p.group_row = g.row;
   p.state_shift = pl.rows_log2;
+  p.state_items = pl.items;
   return run_planned(p, pl.own, workspace, workspace_bytes,
                      [&](int columns) { return launch_attn_own(D, bf16, c->bits, p, columns, s); });
 }

@@ -73,6 +73,7 @@ namespace exl3 {
   }                                                                                                                    \
   hipError_t launch_attn_own_d##D(bool, int, const AttnParams &p, int columns, hipStream_t) {                         \
     need(p.start != nullptr && p.group_of != nullptr && p.group_row != nullptr && p.causal == 1, "own");               \
+    inside(p.state, ((size_t)p.state_items * p.heads_kv << p.state_shift) * (STATE_PAD + D) * 4, "state");            \
     need(p.state_shift == 4 || p.state_shift == 5 || p.state_shift == 7, "rows of the state");                         \
     check_parts(p, columns, D, g_ints);                                                                                \
     ++g_own[columns == 0];                                                                                             \
