@@ -31,7 +31,8 @@
 // of 8000 keys, which then have twice the parts, 38% more); 24 sequences of up
 // to 7 tokens over windows of 4096 keys, 64/8 heads of 64, 131 MB in 41 us, 3.2
 // TB/s (two columns of products and exponentials to a load);
-// one token over 1100 keys, 4.5 MB in 8.9 us.
+// one token over 1100 keys, 4.5 MB in 8.9 us; 32 sequences, one token each, over
+// windows of 4096 and 4 first tokens, 8 bits, 245 MB in 53 us, 4.6 TB/s.
 #pragma once
 
 #include <type_traits>

