@@ -164,6 +164,78 @@ struct Work {
   int item;           // ATTN_PREFIX: the item's number
 };
 
+// ------------------------------------------------- groups that share keys
+//
+// The keys before every new token of a group's sequences, at most prefix_len,
+// are read once for all of them.  Rounded down to a multiple of 32, a step of
+// the attention kernels, so that neither pass has a step of both.  A group with
+// fewer than two sequences that have new tokens shares nothing.
+__device__ __forceinline__ int shared_keys(const GroupsParams &p, int prefix_len, int before, int live) {
+  return live < 2 ? 0 : max(min(min(prefix_len, before), p.table_keys), 0) & ~31;
+}
+
+// The groups as sequences: group g has the rows row[g] .. row[g + 1] - 1 and
+// the page table's row of sequence first[g].
+struct FewGroups {
+  static constexpr int N = FEW_SEQUENCES;
+  int row[N + 1], first[N + 1], keys[N];
+  int seq_row[N + 1], live[N], top[2][4];
+};
+
+// Fewer than 256 sequences: a thread to each, running maxima of the offsets (as
+// find_work has them) and the least of each group, all in LDS after one round of
+// loads.  Every workgroup of the shared keys does it for itself, 3 us before its
+// first key, and one leaves what ATTN_OWN needs: the whole call 81.6 us for 64
+// sequences and 47.0 for 40, with a launch of one workgroup before it 83.2 and 48.6.
+__device__ __forceinline__ void few_groups(const GroupsParams &p, FewGroups &s, bool leave) {
+  constexpr int NONE = 0x7FFFFFFF;
+  const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+  const int row = i <= p.batch ? min(max(p.cu[i], 0), p.tokens) : 0;
+  const int kv = i < p.batch ? p.kv_len[i] : 0;
+  const int seq = i <= p.groups ? min(max(p.group_cu[i], 0), p.batch) : 0;
+  const int prefix_len = i < p.groups ? p.prefix_len[i] : 0;
+  int r = wave_inclusive_max(row), f = wave_inclusive_max(seq);
+  if (lane == 63) s.top[0][wave] = r, s.top[1][wave] = f;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+    if (w < wave) r = max(r, s.top[0][w]), f = max(f, s.top[1][w]);
+  s.seq_row[i] = r;
+  s.first[i] = i <= p.groups ? f : NONE;
+  s.keys[i] = NONE;
+  s.live[i] = 0;
+  __syncthreads();
+  int g = -1;  // the last group that starts at or before the sequence
+  for (int half = 1 << (31 - __builtin_clz(p.groups)); half > 0; half >>= 1)
+    if (s.first[g + half] <= i) g += half;
+  const bool member = i < p.batch && g >= 0 && i < s.first[p.groups];
+  if (member) {
+    const int n = s.seq_row[i + 1] - s.seq_row[i];
+    if (n > 0) {
+      atomicMin(&s.keys[g], max(kv, 0) - n);
+      atomicAdd(&s.live[g], 1);
+    }
+  }
+  __syncthreads();
+  if (i <= p.groups) {
+    s.row[i] = s.seq_row[f];
+    if (i < p.groups) s.keys[i] = shared_keys(p, prefix_len, s.keys[i], s.live[i]);
+    if (leave) p.row[i] = s.row[i];
+  }
+  __syncthreads();
+  if (leave && i < p.batch) {
+    p.start[i] = member ? s.keys[g] : 0;
+    p.of[i] = member ? g : 0;
+  }
+}
+
+// The page table's row for the workgroup's sequence.
+template <int KIND>
+__device__ __forceinline__ int table_row(const AttnParams &p, const Work &w, const FewGroups *few) {
+  if constexpr (KIND == ATTN_PREFIX) return few ? __builtin_amdgcn_readfirstlane(few->first[w.seq]) : p.table_row[w.seq];
+  return w.seq;
+}
+
 // Every wave of the workgroup finds the same answer.  Sequence s has
 // tiles(s) = ceil(q_len * group / R) tiles.  When the call splits keys, those
 // of a sequence whose span (the keys that a tile's rows see at most) exceeds C
@@ -173,7 +245,8 @@ struct Work {
 // lengths that rounding up hits hard; it is at least part_min.  There are
 // never more than tiles + target items, nor 2 * target parts.
 template <int R, int KIND = ATTN_PLAIN>
-__device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w) {
+__device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w,
+                                          const FewGroups *few = nullptr) {
   struct Seq {
     int q0, ql, kv, tiles, span, first;
   };
@@ -183,7 +256,9 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
   auto load = [&](int s0, int &from) __attribute__((always_inline)) -> Seq {
     const int s = s0 + lane;
     int a = 0, b = 0, kv = 0;
-    if (s < p.batch) {
+    if (KIND == ATTN_PREFIX && few) {
+      if (s < p.batch) a = few->row[s], b = few->row[s + 1], kv = few->keys[s];
+    } else if (s < p.batch) {
       a = p.cu[s], b = p.cu[s + 1];
       if (p.kv_len) kv = p.kv_len[s];
     }
@@ -334,9 +409,9 @@ __device__ __forceinline__ KeyRange sink_range(const AttnParams &p, const Work &
 // Every part of a group's tile leaves its rows (m, l, o; nothing is joined
 // there), and the first part of a row's own keys adds them up in a fixed order.
 // What bounds the shared keys is vector work beside the products at 8 bits (matrix
-// units busy 20% of the cycles, vector units 37%) and a start and end of 11 us;
+// units busy 20% of the cycles, vector units 37%) and a start and end of 14 us;
 // the own keys the latency of the longest sequence.  Measured: 64 sequences
-// over 24000 shared and up to 1500 own keys, 32/8 heads of 128, 8 bits: 46 us
+// over 24000 shared and up to 1500 own keys, 32/8 heads of 128, 8 bits: 49 us
 // for the shared keys in 32 parts of 768, 39 for the own, of which 8 are the 34 MB
 // that the parts left.  (Joined by the last part to arrive, as split tiles are
 // below, 24 parts of 66 KB: 72 and 31 us.)

@@ -7,18 +7,20 @@ namespace exl3 {
 
 namespace {
 
+using Params = std::conditional_t<EXL3_KIND == ATTN_PREFIX, PrefixParams, AttnParams>;
+
 // As many workgroups as a plain launch has.
 template <bool BF16, int BITS>
-hipError_t launch_columns(const AttnParams &p, int columns, hipStream_t s) {
+hipError_t launch_columns(const Params &p, int columns, hipStream_t s) {
   const int R = columns > 0 ? 16 * columns : ATTN_TILE_ROWS;
   const dim3 grid = grid_of(((int64_t)p.tokens * p.group / R + p.batch + p.target) * p.heads_kv), block(256);
   if (columns == 0)
-    hipLaunchKernelGGL((attn_tile_kernel<BF16, EXL3_HEAD_DIM, BITS, EXL3_KIND>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((attn_tile_kernel<BF16, EXL3_HEAD_DIM, BITS, EXL3_KIND, Params>), grid, block, 0, s, p);
   else if (columns == 1)
-    hipLaunchKernelGGL((attn_small_kernel<BF16, EXL3_HEAD_DIM, BITS, 1, EXL3_KIND>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((attn_small_kernel<BF16, EXL3_HEAD_DIM, BITS, 1, EXL3_KIND, Params>), grid, block, 0, s, p);
 #if EXL3_HEAD_DIM < 256  // two column tiles of 256-value heads do not fit the registers
   else if (columns == 2)
-    hipLaunchKernelGGL((attn_small_kernel<BF16, EXL3_HEAD_DIM, BITS, 2, EXL3_KIND>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((attn_small_kernel<BF16, EXL3_HEAD_DIM, BITS, 2, EXL3_KIND, Params>), grid, block, 0, s, p);
 #endif
   else
     return hipErrorInvalidValue;
@@ -26,7 +28,7 @@ hipError_t launch_columns(const AttnParams &p, int columns, hipStream_t s) {
 }
 
 template <bool BF16>
-hipError_t launch_bits(int bits, const AttnParams &p, int columns, hipStream_t s) {
+hipError_t launch_bits(int bits, const Params &p, int columns, hipStream_t s) {
   switch (bits) {
 #if EXL3_PACKED
     case 0: return launch_columns<BF16, 0>(p, columns, s);
@@ -40,7 +42,7 @@ hipError_t launch_bits(int bits, const AttnParams &p, int columns, hipStream_t s
 
 }  // namespace
 
-hipError_t EXL3_LAUNCH(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s) {
+hipError_t EXL3_LAUNCH(bool bf16, int bits, const Params &p, int columns, hipStream_t s) {
   return bf16 ? launch_bits<true>(bits, p, columns, s) : launch_bits<false>(bits, p, columns, s);
 }
 

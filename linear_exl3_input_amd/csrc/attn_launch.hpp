@@ -115,6 +115,26 @@ struct AttnParams {
 };
 constexpr int STATE_PAD = 4;  // maximum and sum of a row before its D sums, which stay 16-byte aligned
 
+// What the two passes of attention with shared prefixes need of the groups.
+struct GroupsParams {
+  const int32_t *cu, *kv_len;            // [batch+1], [batch]
+  const int32_t *group_cu, *prefix_len;  // [groups+1], [groups]
+  int32_t batch, tokens, groups, table_keys;
+  int32_t *seq_row;                      // [batch+1] the first row of each sequence
+  int32_t *start;                        // [batch] the first key that is not shared
+  int32_t *first;                        // [groups+1] the first sequence of each group
+  int32_t *row;                          // [groups+1] the first row of each group
+  int32_t *keys;                         // [groups] its shared keys
+  int32_t *of;                           // [batch] the group of each sequence that shares keys
+};
+
+// ATTN_PREFIX: the groups as sequences, which the kernels make themselves (few_groups)
+// for fewer than FEW_SEQUENCES.
+struct PrefixParams : AttnParams {
+  GroupsParams groups;
+};
+constexpr int FEW_SEQUENCES = 256;
+
 // What a kernel computes, apart from the head size, the types and the tiles.
 enum AttnKind {
   ATTN_PLAIN = 0,  // a range of keys for each row
@@ -137,7 +157,7 @@ hipError_t launch_attn_tile(int head_dim, bool bf16, int bits, const AttnParams 
 // ATTN_SINKS; columns as above, 0: tiles of ATTN_TILE_ROWS.
 hipError_t launch_attn_sinks(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
 // ATTN_PREFIX and ATTN_OWN, over a cache.
-hipError_t launch_attn_prefix(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_prefix(int head_dim, bool bf16, int bits, const PrefixParams &p, int columns, hipStream_t s);
 hipError_t launch_attn_own(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
 
 }  // namespace exl3

@@ -149,8 +149,8 @@ __device__ __forceinline__ void store_row(const AttnParams &p, const Work &w, in
   }
 }
 
-template <bool BF16, int D, int BITS, int NT, int KIND = ATTN_PLAIN>
-__global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(AttnParams p) {
+template <bool BF16, int D, int BITS, int NT, int KIND = ATTN_PLAIN, class Params = AttnParams>
+__global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(Params p) {
   constexpr bool PAGED = BITS != 0, SINKS = KIND == ATTN_SINKS;
   constexpr int CB = PAGED ? BITS : 16;  // bits of a stored value
   constexpr int R = 16 * NT;
@@ -169,7 +169,15 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   const int head = workgroup() % p.heads_kv;
   const int item = workgroup() / p.heads_kv;
   Work w;
-  if (!find_work<R, KIND>(p, item, lane, w)) return;
+  __shared__ std::conditional_t<KIND == ATTN_PREFIX, FewGroups, int> s_groups;
+  const FewGroups *few = nullptr;
+  if constexpr (KIND == ATTN_PREFIX) {
+    if (p.groups.batch < FEW_SEQUENCES) {
+      few_groups(p.groups, s_groups, workgroup() == 0);
+      few = &s_groups;
+    }
+  }
+  if (!find_work<R, KIND>(p, item, lane, w, few)) return;
   if (KIND == ATTN_PREFIX && w.kv_len <= 0) return;  // nothing is shared, nothing reads the state
 
   // ---- the tile's rows and their keys
@@ -188,7 +196,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
 
   // ---- where keys and values lie
   const int ps_mask = (1 << p.cache.page_shift) - 1;
-  const int32_t *table = PAGED ? p.page_table + (int64_t)(KIND == ATTN_PREFIX ? p.table_row[w.seq] : w.seq) * p.table_stride
+  const int32_t *table = PAGED ? p.page_table + (int64_t)table_row<KIND>(p, w, few) * p.table_stride
                                : nullptr;
   // lane's keys of a step at k0: first product k0 + 8*(c/4) + c%4 and 4 more,
   // second product k0 + 8*g .. + 7; each within one page (pages hold whole 16s)

@@ -90,8 +90,8 @@ struct TileGeom {
   static constexpr int BUF = K_BYTES + V_BYTES;
 };
 
-template <bool BF16, int D, int BITS, int KIND = ATTN_PLAIN>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnParams p) {
+template <bool BF16, int D, int BITS, int KIND = ATTN_PLAIN, class Params = AttnParams>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Params p) {
   using G = TileGeom<D>;
   constexpr bool PAGED = BITS != 0, SINKS = KIND == ATTN_SINKS;
   constexpr int CB = PAGED ? BITS : 16;
@@ -106,7 +106,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int head = workgroup() % p.heads_kv;
   const int item = workgroup() / p.heads_kv;
   Work w;
-  if (!find_work<R, KIND>(p, item, lane, w)) return;
+  __shared__ std::conditional_t<KIND == ATTN_PREFIX, FewGroups, int> s_groups;
+  const FewGroups *few = nullptr;
+  if constexpr (KIND == ATTN_PREFIX) {
+    if (p.groups.batch < FEW_SEQUENCES) {
+      few_groups(p.groups, s_groups, workgroup() == 0);
+      few = &s_groups;
+    }
+  }
+  if (!find_work<R, KIND>(p, item, lane, w, few)) return;
   if (KIND == ATTN_PREFIX && w.kv_len <= 0) return;  // nothing is shared, nothing reads the state
   const int rows = w.q_len * p.group;
   if constexpr (KIND != ATTN_PREFIX) {
@@ -177,7 +185,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(AttnPa
   const int ka = 4 * (tid / NC), va = 8 * (tid / (2 * NC));
   const int half = (tid / NC) & 1;
   const int ps_mask = (1 << p.cache.page_shift) - 1;
-  const int32_t *table = PAGED ? p.page_table + (int64_t)(KIND == ATTN_PREFIX ? p.table_row[w.seq] : w.seq) * p.table_stride
+  const int32_t *table = PAGED ? p.page_table + (int64_t)table_row<KIND>(p, w, few) * p.table_stride
                                : nullptr;
   auto page_of = [&](int key) __attribute__((always_inline)) -> int {
     const int i = key >> p.cache.page_shift;

@@ -117,18 +117,20 @@ struct PrefixPlan {
 
 // A call whose shared keys, read by every sequence for itself, are fewer bytes
 // than this is paged_attention's: they come from the caches at 8 to 9 TB/s, and
-// the two passes and the groups take 20 us before the first key.  Measured
-// shared / plain, one token, 32/8 heads of 128, 8 bits: 4 sequences of 8192 and
-// 32768 shared keys (54 and 210 MB) 24 / 21 us and 34 / 42, 8 (126, 489) 27 / 25
-// and 39 / 67, 16 (75, 270) 24 / 27 and 28 / 46, 64 of 512 and 2048 (111, 315) 31
-// / 27 and 34 / 48; 8 tokens each, 16 of 8192 (270) 54 / 51; 16 of 16384, 24/4
-// heads of 256, 4 bits (273) 56 / 50.  The host knows the page table's width
-// alone, so that counts as every sequence's keys.
+// the two passes take 16 to 25 us with hardly a key.  Measured shared / plain, one
+// token, 32/8 heads of 128, 8 bits: 4 sequences of 8192 and 32768 shared keys (54
+// and 210 MB) 22 / 21 us and 32 / 42, 8 (126, 489) 25 / 25 and 37 / 67, 16 of 2048
+// and 8192 (75, 270) 22 / 27 and 27 / 46, 64 of 512 and 2048 (111, 315) 29 / 27 and
+// 32 / 47; 8 tokens each, 16 of 8192 (270) 53 / 52.  24/4 heads of 256 need more, at
+// 4 bits 24 sequences of 8192 (213) 55 / 44, 32 (287) 57 / 50 and 64 (583) 66 / 87;
+// 32/8 heads of 256 do not, 16 of 8192 (278) 34 / 50.  The host knows the page
+// table's width alone, so that counts as every sequence's keys.
 constexpr double SHARED_BYTES_MIN = 192e6;
 
 bool worth_sharing(const exl3_kv_cache *c, int32_t page_table_width, int32_t batch, int32_t groups) {
   const double row = c->head_dim * c->bits / 8.0 + (c->bits < 16 ? c->head_dim / 32.0 : 0.0);
-  return (double)(batch - groups) * page_table_width * c->page_size * c->heads * 2 * row >= SHARED_BYTES_MIN;
+  return groups > 0 && (double)(batch - groups) * page_table_width * c->page_size * c->heads * 2 * row >=
+                           SHARED_BYTES_MIN;
 }
 
 exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q_heads, int32_t kv_heads,
@@ -175,11 +177,11 @@ exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q
 
 namespace exl3 {
 
-hipError_t launch_attn_prefix_d64(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
-hipError_t launch_attn_prefix_d128(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
-hipError_t launch_attn_prefix_d256(bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_prefix_d64(bool bf16, int bits, const PrefixParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_prefix_d128(bool bf16, int bits, const PrefixParams &p, int columns, hipStream_t s);
+hipError_t launch_attn_prefix_d256(bool bf16, int bits, const PrefixParams &p, int columns, hipStream_t s);
 
-hipError_t launch_attn_prefix(int head_dim, bool bf16, int bits, const AttnParams &p, int columns, hipStream_t s) {
+hipError_t launch_attn_prefix(int head_dim, bool bf16, int bits, const PrefixParams &p, int columns, hipStream_t s) {
   return head_dim == 64    ? launch_attn_prefix_d64(bf16, bits, p, columns, s)
          : head_dim == 128 ? launch_attn_prefix_d128(bf16, bits, p, columns, s)
                            : launch_attn_prefix_d256(bf16, bits, p, columns, s);
@@ -419,21 +421,21 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
   g.row = take(groups + 1);
   g.keys = take(groups);
   p.group_items = take(2 * (int64_t)groups);
-  if ((st = launched(launch_groups(g, s), "groups launch")) != EXL3_OK) return st;
+  if (batch >= FEW_SEQUENCES && (st = launched(launch_groups(g, s), "groups launch")) != EXL3_OK) return st;
   p.state = reinterpret_cast<float *>(ws + pl.state);
-  if (groups > 0) {
-    AttnParams shared = p;
-    shared.cu = g.row;
-    shared.kv_len = g.keys;
-    shared.table_row = g.first;
-    shared.batch = groups;
-    shared.causal = 0;
-    shared.target = pl.shared.target;
-    shared.part_min = pl.shared.part_min;
-    shared.part_cap = pl.items;
-    st = launched(launch_attn_prefix(D, bf16, c->bits, shared, pl.shared.columns, s), "shared keys launch");
-    if (st != EXL3_OK) return st;
-  }
+  PrefixParams shared;
+  static_cast<AttnParams &>(shared) = p;
+  shared.groups = g;
+  shared.cu = g.row;
+  shared.kv_len = g.keys;
+  shared.table_row = g.first;
+  shared.batch = groups;
+  shared.causal = 0;
+  shared.target = pl.shared.target;
+  shared.part_min = pl.shared.part_min;
+  shared.part_cap = pl.items;
+  st = launched(launch_attn_prefix(D, bf16, c->bits, shared, pl.shared.columns, s), "shared keys launch");
+  if (st != EXL3_OK) return st;
   p.start = g.start;
   p.group_of = g.of;
   p.group_row = g.row;

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attn_launch.hpp"
+
 namespace exl3 {
 
 constexpr int32_t STEP_MAX_LEN = 1 << 30;    // what a kv_len counts as at most
@@ -21,19 +23,7 @@ struct TablesParams {
 
 hipError_t launch_tables(const TablesParams &p, hipStream_t s);
 
-// What the two passes of attention with shared prefixes need of the groups.
-struct GroupsParams {
-  const int32_t *cu, *kv_len;            // [batch+1], [batch]
-  const int32_t *group_cu, *prefix_len;  // [groups+1], [groups]
-  int32_t batch, tokens, groups, table_keys;
-  int32_t *seq_row;                      // [batch+1] the first row of each sequence
-  int32_t *start;                        // [batch] the first key that is not shared
-  int32_t *first;                        // [groups+1] the first sequence of each group
-  int32_t *row;                          // [groups+1] the first row of each group
-  int32_t *keys;                         // [groups] its shared keys
-  int32_t *of;                           // [batch] the group of each sequence that shares keys
-};
-
+// What the kernels of shared keys do for themselves for fewer than FEW_SEQUENCES.
 hipError_t launch_groups(const GroupsParams &p, hipStream_t s);
 
 }  // namespace exl3

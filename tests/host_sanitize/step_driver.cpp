@@ -59,7 +59,7 @@ int main(int argc, char **argv) {
     for (int i = 0; i < 8; ++i) a[i] = std::atoi(argv[i + 1]);
     const size_t n = exl3_prefix_attention_workspace_bytes(a[0], a[1], a[2], a[3], a[4], a[5]);
     if (prefix(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], n) != EXL3_OK) return 1;
-    std::printf("%s %s %s %s\n", g_groups ? "shared" : "plain", g_shared[1] ? "tile" : g_shared[0] ? "small" : "none",
+    std::printf("%s %s %s %s\n", g_shared[0] + g_shared[1] ? "shared" : "plain", g_shared[1] ? "tile" : g_shared[0] ? "small" : "none",
                 g_own[1] ? "tile" : g_own[0] ? "small" : "none", g_split ? "split" : "whole");
     return 0;
   }

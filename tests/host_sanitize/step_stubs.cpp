@@ -47,6 +47,22 @@ void check_parts(const exl3::AttnParams &p, int columns, int D, size_t end) {
   }
   ++g_launches;
 }
+
+void check_groups(const exl3::GroupsParams &p) {
+  need(p.groups > 0 && p.groups <= p.batch, "groups");
+  const struct {
+    const int32_t *at;
+    size_t n;
+  } arrays[] = {{p.seq_row, (size_t)p.batch + 1}, {p.start, (size_t)p.batch},      {p.of, (size_t)p.batch},
+                {p.first, (size_t)p.groups + 1},  {p.row, (size_t)p.groups + 1}, {p.keys, (size_t)p.groups}};
+  size_t before = COUNTERS;
+  g_ints = reinterpret_cast<uintptr_t>(p.seq_row) - g_ws;
+  for (const auto &a : arrays) {
+    need(reinterpret_cast<uintptr_t>(a.at) - g_ws >= before, "arrays apart");
+    before = inside(a.at, 4 * a.n, "arrays in the workspace");
+  }
+  g_ints_end = before;
+}
 }  // namespace
 
 namespace exl3 {
@@ -58,7 +74,9 @@ namespace exl3 {
     ++g_sinks[columns == 0];                                                                                           \
     return hipSuccess;                                                                                                 \
   }                                                                                                                    \
-  hipError_t launch_attn_prefix_d##D(bool, int, const AttnParams &p, int columns, hipStream_t) {                      \
+  hipError_t launch_attn_prefix_d##D(bool, int, const PrefixParams &p, int columns, hipStream_t) {                    \
+    check_groups(p.groups);                                                                                            \
+    need(p.cu == p.groups.row && p.kv_len == p.groups.keys && p.batch == p.groups.groups, "groups as sequences");      \
     const int R = columns ? 16 * columns : ATTN_TILE_ROWS;                                                             \
     need(columns >= 0 && columns <= (D == 256 ? 1 : 2), "columns");                                                    \
     need(p.causal == 0 && p.window == 0 && p.target > 0 && p.part_min >= 128 && p.table_row != nullptr, "shared");     \
@@ -95,19 +113,8 @@ hipError_t launch_tables(const TablesParams &p, hipStream_t) {
   return hipSuccess;
 }
 hipError_t launch_groups(const GroupsParams &p, hipStream_t) {
-  need(p.groups <= p.batch, "groups");
-  const struct {
-    const int32_t *at;
-    size_t n;
-  } arrays[] = {{p.seq_row, (size_t)p.batch + 1}, {p.start, (size_t)p.batch},      {p.of, (size_t)p.batch},
-                {p.first, (size_t)p.groups + 1},  {p.row, (size_t)p.groups + 1}, {p.keys, (size_t)p.groups}};
-  size_t before = COUNTERS;
-  g_ints = reinterpret_cast<uintptr_t>(p.seq_row) - g_ws;
-  for (const auto &a : arrays) {
-    need(reinterpret_cast<uintptr_t>(a.at) - g_ws >= before, "arrays apart");
-    before = inside(a.at, 4 * a.n, "arrays in the workspace");
-  }
-  g_ints_end = before;
+  need(p.batch >= FEW_SEQUENCES, "sequences");
+  check_groups(p);
   ++g_launches, ++g_groups;
   return hipSuccess;
 }

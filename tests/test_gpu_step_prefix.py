@@ -149,6 +149,16 @@ def test_heads_and_members(hq, hkv, members, n, d):
     x.check()
 
 
+@pytest.mark.parametrize("batch", [2, 63, 64, 65, 255, 256, 257])
+def test_groups_of_every_size_by_either_form(batch):
+    """Up to 255 sequences the kernels of the shared keys find the groups themselves: one group, groups of two, and
+    groups with sequences that have no new tokens."""
+    one = Shared([(64, [(1, 1 + i % 20) for i in range(batch)])], 2, 1, 64, BF16, 8, 16, seed=26)
+    one.check()
+    pairs = Shared([(32, [(1, 1 + i % 9), (i % 2, 5)]) for i in range(batch // 2)] + [(32, [])], 2, 1, 64, BF16, 8, 16, seed=27)
+    pairs.check()
+
+
 def test_more_sequences_than_a_workgroup_looks_at_together():
     x = Shared([(48, [(1, 1 + i % 20) for i in range(300)]), (32, [(1, 2)] * 280)], 2, 1, 64, BF16, 16, 16, seed=7)
     x.check()
