@@ -47,9 +47,10 @@ __device__ __forceinline__ void load_floats(const float *a, float (&f)[8]) {
 }
 
 // 1 / sqrt(x), x positive and normal: the instruction's (within a step of its 24
-// bits) and one step of Newton's iteration.  Without it the errors of a whole
-// row go one way, and 12001 tokens' keys, read back from 8 bits, were more than
-// 1.5 times as far from their 64-bit values as with a correctly rounded root.
+// bits) and one step of Newton's iteration, without which a whole row's values are
+// off the same way by up to that step.  With it, of 49 million values 1150 round to
+// the type's other neighbour than in 64 bits; each operation rounded by itself in
+// the order norm, weight, rotation: 1550.
 __device__ __forceinline__ float inverse_root(float x) {
   const float r = __builtin_amdgcn_rsqf(x);
   return __builtin_fmaf(0.5f * r, __builtin_fmaf(-x * r, r, 1.f), r);
