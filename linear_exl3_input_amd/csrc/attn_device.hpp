@@ -247,6 +247,30 @@ __device__ __forceinline__ int table_row(const AttnParams &p, const Work &w, con
 template <int R, int KIND = ATTN_PLAIN>
 __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lane, Work &w,
                                           const FewGroups *few = nullptr) {
+  if (KIND == ATTN_OWN && p.tile_at) {
+    // Whole sequences, and the tiles before each are known: the last one that
+    // starts at or before the item, by 64 of them at a time.  (4000 sequences in 500
+    // groups, the call 225 us; with the scan below, a microsecond for every 64
+    // sequences, 618.)
+    if (item >= p.tile_at[p.batch]) return false;
+    int s = 0;
+    for (int n = p.batch; n > 1;) {
+      const int step = (n + 63) >> 6;
+      const int at = lane * step < n ? p.tile_at[s + lane * step] : 0x7FFFFFFF;
+      const int past = (__builtin_popcountll(__ballot(at <= item)) - 1) * step;
+      s += past;
+      n = min(step, n - past);
+    }
+    w.seq = s;
+    w.tile = item - p.tile_at[s];
+    w.split = w.part = w.part_keys = 0;
+    w.splits = 1;
+    w.q0 = p.seq_row[s];
+    w.q_len = p.seq_row[s + 1] - w.q0;
+    w.kv_len = max(0, p.kv_len[s]);
+    w.first = p.start[s];
+    return true;
+  }
   struct Seq {
     int q0, ql, kv, tiles, span, first;
   };

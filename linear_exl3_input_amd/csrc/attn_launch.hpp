@@ -112,6 +112,9 @@ struct AttnParams {
   const int32_t *group_row;    // and [groups] the first row of each
   int32_t state_shift;         // log2 of a tile's rows there
   int32_t state_items;         // and the items that the state holds
+  // ATTN_OWN, many sequences: [batch+1] the tiles before each sequence, and its
+  // first row (null: found from cu)
+  const int32_t *tile_at, *seq_row;
 };
 constexpr int STATE_PAD = 4;  // maximum and sum of a row before its D sums, which stay 16-byte aligned
 
@@ -126,6 +129,8 @@ struct GroupsParams {
   int32_t *row;                          // [groups+1] the first row of each group
   int32_t *keys;                         // [groups] its shared keys
   int32_t *of;                           // [batch] the group of each sequence that shares keys
+  int32_t *tile_at;                      // [batch+1] the tiles of own keys' rows before each sequence,
+  int32_t group, tile_rows;              // of so many heads a token and rows a tile
 };
 
 // ATTN_PREFIX: the groups as sequences, which the kernels make themselves (few_groups)

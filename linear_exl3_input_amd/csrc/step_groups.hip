@@ -1,65 +1,82 @@
-// Which keys the sequences of a group share.
+// Which keys the sequences of a group share, where they are too many for few_groups.
 #include "step_launch.hpp"
 #include "attn_device.hpp"
 
 namespace exl3 {
 
-// few_groups for any number of sequences, as a launch of one workgroup: running
-// maxima of the offsets, then a wave to a group.  What bounds it is the chain of
-// loads and barriers.
-__global__ __launch_bounds__(256) void groups_kernel(GroupsParams p) {
-  __shared__ int s_top[4];
+// Running maxima of the offsets, and the tiles of own keys' rows before each
+// sequence, by one workgroup, then a wave to a group: two launches of 5 us, whose
+// chains of loads and barriers are what bounds them.  (A wave to a group in the
+// first one's workgroup: 500 groups of two 87 us, 2000 361.)
+__global__ __launch_bounds__(1024) void rising_kernel(GroupsParams p) {
+  constexpr int N = 1024;
+  __shared__ int s_top[3][N / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // to[i] = the largest of from[0..i], each within 0..most
-  auto rising = [&](const int32_t *from, int n, int most, int32_t *to) {
-    int top = 0;
-    for (int i0 = 0; i0 < n; i0 += 256) {
-      const int i = i0 + tid;
-      int v = wave_inclusive_max(i < n ? min(max(from[i], 0), most) : 0);
-      if (lane == 63) s_top[wave] = v;
-      __syncthreads();
-      v = max(v, top);
+  auto row_of = [&](int i) { return i <= p.batch ? min(max(p.cu[i], 0), p.tokens) : 0; };
+  int row_top = 0, first_top = 0, tiles_before = 0;
+  for (int i0 = 0; i0 <= p.batch; i0 += N) {  // (there are at most as many groups)
+    const int i = i0 + tid;
+    const int next = row_of(i + 1);
+    int r = wave_inclusive_max(row_of(i));
+    int f = wave_inclusive_max(i <= p.groups ? min(max(p.group_cu[i], 0), p.batch) : 0);
+    if (lane == 63) s_top[0][wave] = r, s_top[1][wave] = f;
+    __syncthreads();
+    r = max(r, row_top), f = max(f, first_top);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if (w < wave) v = max(v, s_top[w]);
-        top = max(top, s_top[w]);
-      }
-      if (i < n) to[i] = v;
-      __syncthreads();
+    for (int w = 0; w < N / 64; ++w) {
+      const int a = s_top[0][w], b = s_top[1][w];
+      if (w < wave) r = max(r, a), f = max(f, b);
+      row_top = max(row_top, a), first_top = max(first_top, b);
     }
-  };
-  rising(p.cu, p.batch + 1, p.tokens, p.seq_row);
-  rising(p.group_cu, p.groups + 1, p.batch, p.first);
+    const int tiles = i < p.batch ? (int)(((int64_t)max(next - r, 0) * p.group + p.tile_rows - 1) / p.tile_rows) : 0;
+    const int incl = wave_inclusive_sum(tiles);
+    if (lane == 63) s_top[2][wave] = incl;
+    __syncthreads();
+    int before = tiles_before + incl - tiles;
+#pragma unroll
+    for (int w = 0; w < N / 64; ++w) {
+      const int a = s_top[2][w];
+      if (w < wave) before += a;
+      tiles_before += a;
+    }
+    if (i <= p.batch) p.seq_row[i] = r, p.tile_at[i] = before;
+    if (i <= p.groups) p.first[i] = f;
+  }
+}
+
+__global__ __launch_bounds__(256) void groups_kernel(GroupsParams p) {
+  const int tid = blockIdx.x * 256 + threadIdx.x, lane = threadIdx.x & 63, g = tid >> 6;
+  const int step = gridDim.x * 256;
   // sequences of no group
-  for (int s = tid; s < p.first[0]; s += 256) p.start[s] = 0;
-  for (int s = p.first[p.groups] + tid; s < p.batch; s += 256) p.start[s] = 0;
-  for (int g = wave; g < p.groups; g += 4) {
-    const int s0 = p.first[g], s1 = p.first[g + 1];
-    int before = 0x7FFFFFFF, live = 0;  // keys before the first new token; sequences that have one
-    for (int s = s0 + lane; s < s1; s += 64) {
-      const int n = p.seq_row[s + 1] - p.seq_row[s];
-      if (n > 0) {
-        before = min(before, max(p.kv_len[s], 0) - n);
-        ++live;
-      }
-    }
-    live = wave_sum(live);
-    before = 0x7FFFFFFF - __builtin_amdgcn_readlane(wave_inclusive_max(0x7FFFFFFF - max(before, 0)), 63);
-    const int keys = shared_keys(p, p.prefix_len[g], before, live);
-    for (int s = s0 + lane; s < s1; s += 64) {
-      p.start[s] = keys;
-      p.of[s] = g;
-    }
-    if (lane == 0) {
-      p.row[g] = p.seq_row[s0];
-      p.keys[g] = keys;
+  for (int s = tid; s < p.first[0]; s += step) p.start[s] = 0;
+  for (int s = p.first[p.groups] + tid; s < p.batch; s += step) p.start[s] = 0;
+  if (g == p.groups && lane == 0) p.row[g] = p.seq_row[p.first[g]];
+  if (g >= p.groups) return;
+  const int s0 = p.first[g], s1 = p.first[g + 1];
+  int before = 0x7FFFFFFF, live = 0;  // keys before the first new token; sequences that have one
+  for (int s = s0 + lane; s < s1; s += 64) {
+    const int n = p.seq_row[s + 1] - p.seq_row[s];
+    if (n > 0) {
+      before = min(before, max(p.kv_len[s], 0) - n);
+      ++live;
     }
   }
-  if (tid == 0) p.row[p.groups] = p.seq_row[p.first[p.groups]];
+  live = wave_sum(live);
+  before = 0x7FFFFFFF - __builtin_amdgcn_readlane(wave_inclusive_max(0x7FFFFFFF - max(before, 0)), 63);
+  const int keys = shared_keys(p, p.prefix_len[g], before, live);
+  for (int s = s0 + lane; s < s1; s += 64) {
+    p.start[s] = keys;
+    p.of[s] = g;
+  }
+  if (lane == 0) {
+    p.row[g] = p.seq_row[s0];
+    p.keys[g] = keys;
+  }
 }
 
 hipError_t launch_groups(const GroupsParams &p, hipStream_t s) {
-  hipLaunchKernelGGL(groups_kernel, dim3(1), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(rising_kernel, dim3(1), dim3(1024), 0, s, p);
+  hipLaunchKernelGGL(groups_kernel, dim3((p.groups + 4) / 4), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -54,7 +54,8 @@ void check_groups(const exl3::GroupsParams &p) {
     const int32_t *at;
     size_t n;
   } arrays[] = {{p.seq_row, (size_t)p.batch + 1}, {p.start, (size_t)p.batch},      {p.of, (size_t)p.batch},
-                {p.first, (size_t)p.groups + 1},  {p.row, (size_t)p.groups + 1}, {p.keys, (size_t)p.groups}};
+                {p.first, (size_t)p.groups + 1},  {p.row, (size_t)p.groups + 1}, {p.keys, (size_t)p.groups},
+                {p.tile_at, (size_t)p.batch + 1}};
   size_t before = COUNTERS;
   g_ints = reinterpret_cast<uintptr_t>(p.seq_row) - g_ws;
   for (const auto &a : arrays) {
@@ -94,6 +95,7 @@ namespace exl3 {
     inside(p.state, ((size_t)p.state_items * p.heads_kv << p.state_shift) * (STATE_PAD + D) * 4, "state");            \
     need(p.state_shift == 4 || p.state_shift == 5 || p.state_shift == 7, "rows of the state");                         \
     check_parts(p, columns, D, g_ints);                                                                                \
+    need((p.tile_at != nullptr) == (p.batch >= FEW_SEQUENCES) && (p.tile_at == nullptr || p.target == 0), "tiles");    \
     ++g_own[columns == 0];                                                                                             \
     return hipSuccess;                                                                                                 \
   }

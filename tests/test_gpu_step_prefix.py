@@ -159,6 +159,12 @@ def test_groups_of_every_size_by_either_form(batch):
     pairs.check()
 
 
+def test_thousands_of_sequences_some_without_new_tokens():
+    """The own keys' rows of a sequence are found among 4200 by three looks at 64."""
+    x = Shared([(16, [((i + j) % 3, 2 + (i * j) % 7) for j in range(3)]) for i in range(1400)], 2, 1, 64, BF16, 8, 16, seed=28)
+    x.check()
+
+
 def test_more_sequences_than_a_workgroup_looks_at_together():
     x = Shared([(48, [(1, 1 + i % 20) for i in range(300)]), (32, [(1, 2)] * 280)], 2, 1, 64, BF16, 16, 16, seed=7)
     x.check()
