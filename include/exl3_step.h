@@ -91,13 +91,14 @@ exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, 
 /* exl3_paged_attention (without a window) of sequences that share prefixes.
  * Group g is the sequences group_cu[g] .. group_cu[g+1]-1 (int32 [groups+1],
  * non-decreasing, from 0 to batch; at most as many groups as sequences;
- * sequences of no group share nothing), whose rows of the page table have the same pages for their first prefix_len[g]
+ * sequences of no group share nothing), whose rows of the page table, but for
+ * sequences without new tokens, have the same pages for their first prefix_len[g]
  * (int32 [groups]) keys.  Of those, the keys before every new token of the
- * group's sequences are read once for all of them, by way of the first one's
- * row of the table; the result is exl3_paged_attention's but for the order of
- * sums.  Calls that gain nothing by it, by their sizes (few sequences or a narrow
- * page table), are one launch of that, others three.  An offset in group_cu counts as at least those before it
- * and at most batch. */
+ * group's sequences are read once for all of them; the result is
+ * exl3_paged_attention's but for the order of sums.  Calls that gain nothing by
+ * it, by their sizes (few sequences or a narrow page table), are one launch of
+ * that, others two, or four of 256 sequences and more.  An offset in group_cu
+ * counts as at least those before it and at most batch. */
 exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
                                   const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
                                   int64_t page_table_stride, int32_t page_table_width, int32_t batch, int32_t tokens,

@@ -632,8 +632,9 @@ def prefix_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len
     """paged_attention of sequences that share prefixes, whose keys and values are read once for all that share them.
 
     Group g is the sequences group_cu[g]..group_cu[g+1]-1 (int32 [groups+1]); their rows of the page table have the same
-    pages for their first prefix_len[g] keys (int32 [groups]).  Sequences of no group share nothing.  The rest is
-    paged_attention's, and so is the result but for the order of sums."""
+    pages for their first prefix_len[g] keys (int32 [groups]; rows of sequences without new tokens may hold anything).
+    Sequences of no group share nothing.  The rest is paged_attention's, and so is the result but for the order of
+    sums."""
     if _current_device() != cache.device.index:
         with torch.cuda.device(cache.device):
             return prefix_attention(cache, q, cu_q, kv_len, page_table, group_cu, prefix_len, scale, out)

@@ -169,17 +169,18 @@ struct Work {
 // The keys before every new token of a group's sequences, at most prefix_len,
 // are read once for all of them.  Rounded down to a multiple of 32, a step of
 // the attention kernels, so that neither pass has a step of both.  A group with
-// fewer than two sequences that have new tokens shares nothing.
-__device__ __forceinline__ int shared_keys(const GroupsParams &p, int prefix_len, int before, int live) {
-  return live < 2 ? 0 : max(min(min(prefix_len, before), p.table_keys), 0) & ~31;
+// fewer than two sequences that have new tokens shares nothing; those without
+// any count for nothing, and their pages may be gone.
+__device__ __forceinline__ int shared_keys(const GroupsParams &p, int prefix_len, int before, bool two) {
+  return !two ? 0 : max(min(min(prefix_len, before), p.table_keys), 0) & ~31;
 }
 
 // The groups as sequences: group g has the rows row[g] .. row[g + 1] - 1 and
-// the page table's row of sequence first[g].
+// the page table's row of sequence lead[g], the first that has new tokens.
 struct FewGroups {
   static constexpr int N = FEW_SEQUENCES;
-  int row[N + 1], first[N + 1], keys[N];
-  int seq_row[N + 1], live[N], top[2][4];
+  int row[N + 1], keys[N], lead[N];
+  int seq_row[N + 1], first[N + 1], last[N], top[2][4];
 };
 
 // Fewer than 256 sequences: a thread to each, running maxima of the offsets (as
@@ -203,7 +204,8 @@ __device__ __forceinline__ void few_groups(const GroupsParams &p, FewGroups &s, 
   s.seq_row[i] = r;
   s.first[i] = i <= p.groups ? f : NONE;
   s.keys[i] = NONE;
-  s.live[i] = 0;
+  s.lead[i] = NONE;
+  s.last[i] = -1;
   __syncthreads();
   int g = -1;  // the last group that starts at or before the sequence
   for (int half = 1 << (31 - __builtin_clz(p.groups)); half > 0; half >>= 1)
@@ -213,13 +215,14 @@ __device__ __forceinline__ void few_groups(const GroupsParams &p, FewGroups &s, 
     const int n = s.seq_row[i + 1] - s.seq_row[i];
     if (n > 0) {
       atomicMin(&s.keys[g], max(kv, 0) - n);
-      atomicAdd(&s.live[g], 1);
+      atomicMin(&s.lead[g], i);
+      atomicMax(&s.last[g], i);
     }
   }
   __syncthreads();
   if (i <= p.groups) {
     s.row[i] = s.seq_row[f];
-    if (i < p.groups) s.keys[i] = shared_keys(p, prefix_len, s.keys[i], s.live[i]);
+    if (i < p.groups) s.keys[i] = shared_keys(p, prefix_len, s.keys[i], s.lead[i] < s.last[i]);
     if (leave) p.row[i] = s.row[i];
   }
   __syncthreads();
@@ -232,7 +235,7 @@ __device__ __forceinline__ void few_groups(const GroupsParams &p, FewGroups &s, 
 // The page table's row for the workgroup's sequence.
 template <int KIND>
 __device__ __forceinline__ int table_row(const AttnParams &p, const Work &w, const FewGroups *few) {
-  if constexpr (KIND == ATTN_PREFIX) return few ? __builtin_amdgcn_readfirstlane(few->first[w.seq]) : p.table_row[w.seq];
+  if constexpr (KIND == ATTN_PREFIX) return few ? __builtin_amdgcn_readfirstlane(few->lead[w.seq]) : p.table_row[w.seq];
   return w.seq;
 }
 

@@ -128,6 +128,7 @@ struct GroupsParams {
   int32_t *first;                        // [groups+1] the first sequence of each group
   int32_t *row;                          // [groups+1] the first row of each group
   int32_t *keys;                         // [groups] its shared keys
+  int32_t *lead;                         // [groups] the sequence by whose row of the page table they are read
   int32_t *of;                           // [batch] the group of each sequence that shares keys
   int32_t *tile_at;                      // [batch+1] the tiles of own keys' rows before each sequence,
   int32_t group, tile_rows;              // of so many heads a token and rows a tile

@@ -43,7 +43,7 @@
 // GFLOP in 690-735 us, 710-760; windows of 2048, 24/4 heads of 256, 206 GFLOP in
 // 277-295 us, 700-745 (one wave a SIMD, as o alone takes 128 registers); with 16
 // first tokens beside windows of 1024, 305 GFLOP in 471 us, 648; chunks of up to 900
-// tokens over windows of 2048 and 100 first tokens, heads of 128, 67 GFLOP in 92, 733.
+// tokens over windows of 2048 and 100 first tokens, heads of 128, 67 GFLOP in 92-97, 700-733.
 // Registers are short: two waves a SIMD have 256 each, which heads of 64 and
 // 128 fill; over codes and with heads of 64 over 16-bit caches 1 to 14 registers
 // are kept in memory, elsewhere none.  64 rows a wave halve the LDS reads but

@@ -53,17 +53,20 @@ __global__ __launch_bounds__(256) void groups_kernel(GroupsParams p) {
   if (g == p.groups && lane == 0) p.row[g] = p.seq_row[p.first[g]];
   if (g >= p.groups) return;
   const int s0 = p.first[g], s1 = p.first[g + 1];
-  int before = 0x7FFFFFFF, live = 0;  // keys before the first new token; sequences that have one
+  int before = 0x7FFFFFFF, live = 0, lead = 0x7FFFFFFF;  // keys before the first new token; sequences that have one
   for (int s = s0 + lane; s < s1; s += 64) {
     const int n = p.seq_row[s + 1] - p.seq_row[s];
     if (n > 0) {
       before = min(before, max(p.kv_len[s], 0) - n);
+      lead = min(lead, s);
       ++live;
     }
   }
   live = wave_sum(live);
-  before = 0x7FFFFFFF - __builtin_amdgcn_readlane(wave_inclusive_max(0x7FFFFFFF - max(before, 0)), 63);
-  const int keys = shared_keys(p, p.prefix_len[g], before, live);
+  auto least = [](int v) { return 0x7FFFFFFF - __builtin_amdgcn_readlane(wave_inclusive_max(0x7FFFFFFF - max(v, 0)), 63); };
+  before = least(before);
+  lead = least(lead);
+  const int keys = shared_keys(p, p.prefix_len[g], before, live > 1);
   for (int s = s0 + lane; s < s1; s += 64) {
     p.start[s] = keys;
     p.of[s] = g;
@@ -71,6 +74,7 @@ __global__ __launch_bounds__(256) void groups_kernel(GroupsParams p) {
   if (lane == 0) {
     p.row[g] = p.seq_row[s0];
     p.keys[g] = keys;
+    p.lead[g] = lead;  // (none: keys is 0)
   }
 }
 

@@ -164,7 +164,7 @@ exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q
   pl->items = (int32_t)items;
   auto whole = [](size_t n) { return (n + 255) & ~(size_t)255; };
   pl->ints = whole(std::max(pl->own.workspace, (size_t)EXL3_WORKSPACE_COUNTER_BYTES));
-  pl->state = pl->ints + whole(sizeof(int32_t) * (4 * (size_t)batch + 2 + 5 * (size_t)groups + 2));
+  pl->state = pl->ints + whole(sizeof(int32_t) * (4 * (size_t)batch + 2 + 6 * (size_t)groups + 2));
   AttnPlan plain;  // a call that is not worth it
   if ((st = plan_attention(batch, tokens, q_heads, kv_heads, head_dim, &plain)) != EXL3_OK) return st;
   pl->workspace =
@@ -420,6 +420,7 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
   g.first = take(groups + 1);
   g.row = take(groups + 1);
   g.keys = take(groups);
+  g.lead = take(groups);
   g.tile_at = take(batch + 1);
   g.group = p.group;
   g.tile_rows = tile_rows(pl.own.columns);
@@ -431,7 +432,7 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
   shared.groups = g;
   shared.cu = g.row;
   shared.kv_len = g.keys;
-  shared.table_row = g.first;
+  shared.table_row = g.lead;
   shared.batch = groups;
   shared.causal = 0;
   shared.target = pl.shared.target;

@@ -54,7 +54,7 @@ void check_groups(const exl3::GroupsParams &p) {
     const int32_t *at;
     size_t n;
   } arrays[] = {{p.seq_row, (size_t)p.batch + 1}, {p.start, (size_t)p.batch},      {p.of, (size_t)p.batch},
-                {p.first, (size_t)p.groups + 1},  {p.row, (size_t)p.groups + 1}, {p.keys, (size_t)p.groups},
+                {p.first, (size_t)p.groups + 1},  {p.row, (size_t)p.groups + 1}, {p.keys, (size_t)p.groups},       {p.lead, (size_t)p.groups},
                 {p.tile_at, (size_t)p.batch + 1}};
   size_t before = COUNTERS;
   g_ints = reinterpret_cast<uintptr_t>(p.seq_row) - g_ws;

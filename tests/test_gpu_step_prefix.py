@@ -165,6 +165,17 @@ def test_thousands_of_sequences_some_without_new_tokens():
     x.check()
 
 
+@pytest.mark.parametrize("others", [0, 260])
+def test_ended_sequences_whose_pages_are_gone(others):
+    """A server's slots that hold no request: no new tokens, and a row of the page table without pages or with others'."""
+    x = Shared([(96, [(0, 5), (1, 9), (0, 3), (2, 60), (1, 1), (0, 7)]), (64, [(0, 1), (0, 2)]), (48, [(0, 1), (1, 9), (3, 3)]),
+                (32, [(0, 1), (1, 9)])] + [(16, [(1, 2)] * others)] * (others > 0), 4, 2, 64, BF16, 8, 16, seed=29)
+    for s in (0, 2, 5, 6, 8, 11):
+        x.table[s] = -1 if s % 2 == 0 else 1
+        x.kv_lens[s] = 0 if s % 4 == 0 else 40
+    x.check()
+
+
 def test_more_sequences_than_a_workgroup_looks_at_together():
     x = Shared([(48, [(1, 1 + i % 20) for i in range(300)]), (32, [(1, 2)] * 280)], 2, 1, 64, BF16, 16, 16, seed=7)
     x.check()
