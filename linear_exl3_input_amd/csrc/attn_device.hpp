@@ -149,6 +149,17 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits(), 63));
 }
 
+// What the kind settles, so that the compiler knows it (64 sequences over 24000
+// shared keys 81.9 -> 80.9 us, 40 of questions 46.5 -> 45.7).
+template <int KIND>
+__device__ __forceinline__ int causal_of(const AttnParams &p) {
+  return KIND == ATTN_PREFIX ? 0 : KIND == ATTN_OWN ? 1 : p.causal;
+}
+template <int KIND>
+__device__ __forceinline__ int window_of(const AttnParams &p) {
+  return KIND == ATTN_PREFIX || KIND == ATTN_OWN ? 0 : p.window;
+}
+
 // One workgroup's work: rows [tile * R, ...) of a sequence's q_len * group
 // rows on one key/value head, and its part of their keys.  Row r is head
 // r % group of new token r / group: the heads that share keys and values are
@@ -303,7 +314,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
       x.first = s < p.batch ? p.start[s] : 0;
       x.span = max(0, x.span - (x.first & ~31));
     }
-    if (p.window > 0) x.span = min(x.span, p.window + R + 32 + (KIND == ATTN_SINKS ? p.sink_keys : 0));
+    if (window_of<KIND>(p) > 0) x.span = min(x.span, window_of<KIND>(p) + R + 32 + (KIND == ATTN_SINKS ? p.sink_keys : 0));
     return x;
   };
   int head_end = 0, from;
@@ -387,9 +398,9 @@ __device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w
   k.shift = w.kv_len - w.q_len;
   k.p_first = k.shift + quotient(r0, p.by_group);
   k.p_last = k.shift + quotient(r_last, p.by_group);
-  k.hi = p.causal ? min(w.kv_len, k.p_last + 1) : w.kv_len;
+  k.hi = causal_of<KIND>(p) ? min(w.kv_len, k.p_last + 1) : w.kv_len;
   if (p.kv_len) k.hi = min(k.hi, p.table_keys);  // past the table everything is a hole
-  k.lo = p.window > 0 ? max(0, k.p_first - p.window + 1) : 0;
+  k.lo = window_of<KIND>(p) > 0 ? max(0, k.p_first - window_of<KIND>(p) + 1) : 0;
   if constexpr (KIND == ATTN_OWN) k.lo = w.first;
   if (w.splits > 1) {
     const int64_t from = (int64_t)(k.lo & ~31) + (int64_t)w.split * w.part_keys;

@@ -227,8 +227,8 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
     const int i = quotient(live[n] ? r : r_last, p.by_group);
     const int h = (live[n] ? r : r_last) - i * p.group;
     const int pos = shift + i;
-    first[n] = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
-    span[n] = max(0, (p.causal ? min(hi, pos + 1) : hi) - first[n]);
+    first[n] = window_of<KIND>(p) > 0 ? max(lo, pos - window_of<KIND>(p) + 1) : lo;
+    span[n] = max(0, (causal_of<KIND>(p) ? min(hi, pos + 1) : hi) - first[n]);
     sink[n] = SINKS ? min(kr.sinks, pos + 1) : 0;
     q_row[n] = p.q.data + (int64_t)(w.q0 + i) * p.q.token + (int64_t)(head * p.group + h) * p.q.head;
   }
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(256, D * NT >= 256 ? 1 : 2) void attn_small_kernel(
   // whether every row sees every key of the step at k (holes aside)
   auto whole_step = [&](int k) __attribute__((always_inline)) {
     if (SINKS && k + 32 <= min(kr.sinks, p_first + 1)) return true;
-    return k >= lo && k + 32 <= hi && (!p.causal || k + 31 <= p_first) && (p.window == 0 || k > p_last - p.window);
+    return k >= lo && k + 32 <= hi && (!causal_of<KIND>(p) || k + 31 <= p_first) && (window_of<KIND>(p) == 0 || k > p_last - window_of<KIND>(p));
   };
 
   float4_t o[NT][DV];

@@ -143,13 +143,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Params
   // ---- the lane's row, which sees the keys first .. first + span - 1
   const int row = r0 + 32 * wave + col;
   const int pos = shift + quotient(min(row, r_last), p.by_group);
-  const int first = p.window > 0 ? max(lo, pos - p.window + 1) : lo;
-  const int span = max(0, (p.causal ? min(hi, pos + 1) : hi) - first);
+  const int first = window_of<KIND>(p) > 0 ? max(lo, pos - window_of<KIND>(p) + 1) : lo;
+  const int span = max(0, (causal_of<KIND>(p) ? min(hi, pos + 1) : hi) - first);
   const int sink = SINKS ? min(kr.sinks, pos + 1) : 0;  // and, with SINKS, 0 .. sink - 1
   // of the wave's rows, first to last, every one sees [w_lo, w_hi)
   const int wp0 = shift + quotient(min(r0 + 32 * wave, r_last), p.by_group);
   const int wp1 = shift + quotient(min(r0 + 32 * wave + 31, r_last), p.by_group);
-  const int w_hi = p.causal ? min(hi, wp0 + 1) : hi, w_lo = p.window > 0 ? max(lo, wp1 - p.window + 1) : lo;
+  const int w_hi = causal_of<KIND>(p) ? min(hi, wp0 + 1) : hi, w_lo = window_of<KIND>(p) > 0 ? max(lo, wp1 - window_of<KIND>(p) + 1) : lo;
   const int w_sink = SINKS ? min(kr.sinks, wp0 + 1) : 0;
   // Whole rows pass between memory and the wave's registers through its quarter
   // of LDS (before the first and after the last tile): a row's D / 8 pieces by
@@ -296,8 +296,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Params
   auto whole_tile = [&](int t) __attribute__((always_inline)) {
     const int k0 = tile_key(t);
     if (SINKS && k0 + BN <= min(kr.sinks, p_first + 1)) return !holes;
-    return k0 >= lo && k0 + BN <= hi && (!p.causal || k0 + BN - 1 <= p_first) &&
-           (p.window == 0 || k0 > p_last - p.window) && !holes;
+    return k0 >= lo && k0 + BN <= hi && (!causal_of<KIND>(p) || k0 + BN - 1 <= p_first) &&
+           (window_of<KIND>(p) == 0 || k0 > p_last - window_of<KIND>(p)) && !holes;
   };
   // Piece i (0..3) of the thread's keys to tile t's buffer.
   auto put_k = [&](int t, int i) __attribute__((always_inline)) {
