@@ -96,7 +96,8 @@ exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, 
  * (int32 [groups]) keys.  Of those, the keys before every new token of the
  * group's sequences are read once for all of them; the result is
  * exl3_paged_attention's but for the order of sums.  Calls that gain nothing by
- * it, by their sizes (few sequences or a narrow page table), are one launch of
+ * it, by their sizes (few sequences, a narrow page table or more than 512 rows of a
+ * sequence on each key/value head, on average), are one launch of
  * that, others two, or four of 256 sequences and more.  An offset in group_cu
  * counts as at least those before it and at most batch. */
 exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,

@@ -113,6 +113,7 @@ struct PrefixPlan {
   int32_t items;         // of the shared keys, at most, on each key/value head
   int32_t rows_log2;     // rows of an item
   size_t ints, state, workspace;  // offsets
+  bool shares;           // else the call is paged_attention's, whatever it is given
 };
 
 // A call whose shared keys, read by every sequence for itself, are fewer bytes
@@ -127,6 +128,13 @@ struct PrefixPlan {
 // table's width alone, so that counts as every sequence's keys.
 constexpr double SHARED_BYTES_MIN = 192e6;
 
+// And so is a call whose sequences fill the tile kernel's tiles by themselves, for
+// what every tile leaves costs more than the keys: by the average rows of a
+// sequence on a key/value head, over 8192 shared keys, shared / plain, 256 rows
+// 180 / 212 us, 512 275 / 270 (64 sequences 828 / 925), 1024 520 / 434 (24/4 heads of
+// 256, 1536 rows 780 / 838), 2048 850 / 838.  It also bounds the workspace.
+constexpr int64_t SHARED_ROWS_MAX = 512;
+
 bool worth_sharing(const exl3_kv_cache *c, int32_t page_table_width, int32_t batch, int32_t groups) {
   const double row = c->head_dim * c->bits / 8.0 + (c->bits < 16 ? c->head_dim / 32.0 : 0.0);
   return groups > 0 && (double)(batch - groups) * page_table_width * c->page_size * c->heads * 2 * row >=
@@ -138,6 +146,11 @@ exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q
   exl3_status st;
   if (groups < 0 || groups > batch)
     return host_fail(EXL3_ERR_INVALID_ARG, "groups=%d, must be 0..batch=%d", groups, batch);
+  AttnPlan plain;  // a call that is not worth it
+  if ((st = plan_attention(batch, tokens, q_heads, kv_heads, head_dim, &plain)) != EXL3_OK) return st;
+  pl->workspace = std::max(plain.workspace, (size_t)EXL3_WORKSPACE_COUNTER_BYTES);
+  pl->shares = (int64_t)tokens * (q_heads / kv_heads) <= SHARED_ROWS_MAX * batch;
+  if (!pl->shares) return EXL3_OK;
   // Own keys: 16 rows a workgroup rather than 32, since each of them reads what
   // the shared keys left for its rows (16 sequences of 8 tokens, 8 heads of 128:
   // 19 us, with 32 rows 29), and in parts only where whole sequences do not
@@ -165,11 +178,9 @@ exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q
   auto whole = [](size_t n) { return (n + 255) & ~(size_t)255; };
   pl->ints = whole(std::max(pl->own.workspace, (size_t)EXL3_WORKSPACE_COUNTER_BYTES));
   pl->state = pl->ints + whole(sizeof(int32_t) * (4 * (size_t)batch + 2 + 6 * (size_t)groups + 2));
-  AttnPlan plain;  // a call that is not worth it
-  if ((st = plan_attention(batch, tokens, q_heads, kv_heads, head_dim, &plain)) != EXL3_OK) return st;
-  pl->workspace =
-      pl->state + sizeof(float) * ((size_t)pl->items * kv_heads << pl->rows_log2) * (STATE_PAD + head_dim);
-  pl->workspace = std::max(pl->workspace, plain.workspace);
+  pl->workspace = std::max(
+      pl->workspace,
+      pl->state + sizeof(float) * ((size_t)pl->items * kv_heads << pl->rows_log2) * (STATE_PAD + head_dim));
   return EXL3_OK;
 }
 
@@ -392,7 +403,7 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
     return host_fail(EXL3_ERR_WORKSPACE, "workspace of %zu bytes; this call needs %zu (short by %zu)", workspace_bytes,
                      pl.workspace, pl.workspace > workspace_bytes ? pl.workspace - workspace_bytes : (size_t)0);
   if ((st = check_ptr(workspace, "workspace")) != EXL3_OK) return st;
-  if (!worth_sharing(c, page_table_width, batch, groups))
+  if (!pl.shares || !worth_sharing(c, page_table_width, batch, groups))
     return exl3_paged_attention(c, q, out, cu_q, kv_len, page_table, page_table_stride, page_table_width, batch, tokens,
                                 scale, 0, workspace, workspace_bytes, stream);
   const hipStream_t s = (hipStream_t)stream;

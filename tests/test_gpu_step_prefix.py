@@ -159,6 +159,13 @@ def test_groups_of_every_size_by_either_form(batch):
     pairs.check()
 
 
+@pytest.mark.parametrize("n", [128, 129])
+def test_chunks_up_to_and_past_what_is_shared(n):
+    """512 rows of a sequence on each key/value head are the most that the shared passes take."""
+    x = Shared([(224, [(n, n + 30), (n, n + 1)])], 8, 2, 128, BF16, 8, 16, seed=30)
+    x.check()
+
+
 def test_thousands_of_sequences_some_without_new_tokens():
     """The own keys' rows of a sequence are found among 4200 by three looks at 64."""
     x = Shared([(16, [((i + j) % 3, 2 + (i * j) % 7) for j in range(3)]) for i in range(1400)], 2, 1, 64, BF16, 8, 16, seed=28)

@@ -50,7 +50,9 @@ def test_step_host_code_under_sanitizers(driver):
     ((64, 64, 64, 32, 8, 128, 8, 1600), "plain none none whole"),    # a group to each sequence
     ((8, 8, 1, 32, 8, 128, 8, 4000), "shared small small split"),
     ((3, 210, 1, 32, 8, 128, 16, 6000), "shared tile tile split"),
-    ((16, 16, 1, 24, 4, 256, 4, 6000), "shared small small split")])
+    ((16, 16, 1, 24, 4, 256, 4, 6000), "shared small small split"),
+    ((16, 2048, 1, 32, 8, 128, 8, 6000), "shared tile tile split"),  # 512 rows of a sequence on each key/value head
+    ((16, 2052, 1, 32, 8, 128, 8, 6000), "plain none none whole")])  # and 513
 def test_the_passes_of_a_call_with_shared_prefixes(driver, sizes, want):
     assert driver(*sizes).split() == want.split()
 
