@@ -166,6 +166,14 @@ def test_chunks_up_to_and_past_what_is_shared(n):
     x.check()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_hundreds_of_sequences_with_tiles_of_rows(d):
+    """Own keys by the kernel of many rows, one and two tiles of a sequence, found among 270 sequences."""
+    x = Shared([(48, [((0, 20, 37, 23)[i % 4], 40 + i % 11) for i in range(200)]), (16, [(21, 30 + i) for i in range(70)])], 8, 2, d,
+               BF16, 8, 16, seed=31)
+    x.check()
+
+
 def test_thousands_of_sequences_some_without_new_tokens():
     """The own keys' rows of a sequence are found among 4200 by three looks at 64."""
     x = Shared([(16, [((i + j) % 3, 2 + (i * j) % 7) for j in range(3)]) for i in range(1400)], 2, 1, 64, BF16, 8, 16, seed=28)
