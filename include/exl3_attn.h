@@ -114,10 +114,11 @@ exl3_status exl3_cache_read(const exl3_kv_cache *c, const int32_t *slots, int32_
  * p-window+1..p when window > 0 (at most 2^30).  Key j is at offset
  * j % page_size of page page_table[s][j / page_size] (int32, row stride
  * page_table_stride, width page_table_width); a page outside 0..pages-1, or
- * past the width, is a hole whose keys nobody sees.  Query head h reads the
- * cache's head h / (q.heads / heads).  Rows that see no key are zero.  An
- * offset in cu_q counts as at least those before it and at most tokens; rows
- * that then belong to no sequence are not written.
+ * past the width, is a hole whose keys nobody sees.  A length in kv_len counts
+ * as 0 to 2^31 - 2^16.  Query head h reads the cache's head
+ * h / (q.heads / heads).  Rows that see no key are zero.  An offset in cu_q
+ * counts as at least those before it and at most tokens; rows that then belong
+ * to no sequence are not written.
  *   out = softmax(scale * q k^T) v, products in the cache's dtype with fp32
  * sums, the probabilities rounded to that type for the second product.  out is
  * either exactly q (same pointer and strides: in place) or does not overlap q;

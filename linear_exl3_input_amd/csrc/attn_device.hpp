@@ -2,7 +2,7 @@
 // cache's codes and scales, and the assignment of work to workgroups.
 #pragma once
 
-#include "attn_launch.hpp"
+#include "attn_ranges.hpp"
 #include "exl3_device.hpp"
 
 namespace exl3 {
@@ -81,10 +81,6 @@ __device__ __forceinline__ float prob_base(float m) {
 // The workgroup's number in a grid of grid_of.
 __device__ __forceinline__ uint32_t workgroup() { return blockIdx.y << GRID_X_LOG2 | blockIdx.x; }
 
-__device__ __forceinline__ int quotient(int n, const Divisor &d) {
-  return d.mul == 0u ? n : (int)(__umulhi((uint32_t)n, d.mul) >> d.shift);
-}
-
 // ------------------------------------------------------- codes and scales
 
 // The scale of byte s as a float: 2^(s - 127).  255, a block that held a NaN
@@ -149,32 +145,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits(), 63));
 }
 
-// What the kind settles, so that the compiler knows it (64 sequences over 24000
-// shared keys 81.9 -> 80.9 us, 40 of questions 46.5 -> 45.7).
-template <int KIND>
-__device__ __forceinline__ int causal_of(const AttnParams &p) {
-  return KIND == ATTN_PREFIX ? 0 : KIND == ATTN_OWN ? 1 : p.causal;
-}
-template <int KIND>
-__device__ __forceinline__ int window_of(const AttnParams &p) {
-  return KIND == ATTN_PREFIX || KIND == ATTN_OWN ? 0 : p.window;
-}
-
-// One workgroup's work: rows [tile * R, ...) of a sequence's q_len * group
-// rows on one key/value head, and its part of their keys.  Row r is head
-// r % group of new token r / group: the heads that share keys and values are
-// one tile's rows.
-struct Work {
-  int seq, tile;
-  int split, splits;  // this part of the tile's keys, of how many
-  int part_keys;      // keys of a part (splits > 1)
-  int q0, q_len;      // the sequence's first query row and their number
-  int kv_len;
-  int part;           // splits > 1: the part's number among those of all split tiles
-  int first;          // ATTN_OWN: the first key
-  int item;           // ATTN_PREFIX: the item's number
-};
-
 // ------------------------------------------------- groups that share keys
 //
 // The keys before every new token of a group's sequences, at most prefix_len,
@@ -225,7 +195,7 @@ __device__ __forceinline__ void few_groups(const GroupsParams &p, FewGroups &s, 
   if (member) {
     const int n = s.seq_row[i + 1] - s.seq_row[i];
     if (n > 0) {
-      atomicMin(&s.keys[g], max(kv, 0) - n);
+      atomicMin(&s.keys[g], counted_keys(kv) - n);
       atomicMin(&s.lead[g], i);
       atomicMax(&s.last[g], i);
     }
@@ -281,7 +251,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
     w.splits = 1;
     w.q0 = p.seq_row[s];
     w.q_len = p.seq_row[s + 1] - w.q0;
-    w.kv_len = max(0, p.kv_len[s]);
+    w.kv_len = counted_keys(p.kv_len[s]);
     w.first = p.start[s];
     return true;
   }
@@ -306,7 +276,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
     Seq x;
     x.q0 = a;
     x.ql = b - a;
-    x.kv = p.kv_len ? max(0, kv) : x.ql;
+    x.kv = p.kv_len ? counted_keys(kv) : x.ql;
     x.tiles = (int)(((int64_t)x.ql * p.group + R - 1) / R);
     // a tile's rows are at most R tokens; its keys start at a multiple of 32
     x.span = p.kv_len ? min(x.kv, p.table_keys) : x.kv;
@@ -380,63 +350,6 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
     pbase += __builtin_amdgcn_readlane(pincl, 63);
   }
   return false;
-}
-
-// The keys that a workgroup reads, [lo, hi), of those the tile's rows r0 ..
-// r_last see, and the multiple of 32 where it starts.
-struct KeyRange {
-  int shift;            // a new token's position is its index + shift
-  int p_first, p_last;  // positions of the first and the last row
-  int start, lo, hi;
-  int end;              // where the workgroup's steps end: hi, but see sink_range
-  int sinks, sink_end, skip;
-};
-
-template <int KIND = ATTN_PLAIN>
-__device__ __forceinline__ KeyRange key_range(const AttnParams &p, const Work &w, int r0, int r_last) {
-  KeyRange k;
-  k.shift = w.kv_len - w.q_len;
-  k.p_first = k.shift + quotient(r0, p.by_group);
-  k.p_last = k.shift + quotient(r_last, p.by_group);
-  k.hi = causal_of<KIND>(p) ? min(w.kv_len, k.p_last + 1) : w.kv_len;
-  if (p.kv_len) k.hi = min(k.hi, p.table_keys);  // past the table everything is a hole
-  k.lo = window_of<KIND>(p) > 0 ? max(0, k.p_first - window_of<KIND>(p) + 1) : 0;
-  if constexpr (KIND == ATTN_OWN) k.lo = w.first;
-  if (w.splits > 1) {
-    const int64_t from = (int64_t)(k.lo & ~31) + (int64_t)w.split * w.part_keys;
-    k.lo = (int)min<int64_t>(max<int64_t>(from, k.lo), MAX_KEYS);
-    k.hi = (int)min<int64_t>(from + w.part_keys, k.hi);
-  }
-  k.start = k.lo & ~31;
-  k.end = k.hi;
-  return k;
-}
-
-// The same for rows that see a window, lo .. of the first row to hi, and the
-// first `sinks` keys.  Steps of whole tiles of G keys go over places: the first
-// keys' tiles, then from the multiple of 32 at or below lo on; place x from
-// sink_end on is key x + skip.  (Where those tiles reach the window, every place
-// is its key.)  Parts are ranges of places; lo and hi stay those of the tile.
-template <int G>
-__device__ __forceinline__ KeyRange sink_range(const AttnParams &p, const Work &w, int r0, int r_last) {
-  KeyRange k;
-  k.shift = w.kv_len - w.q_len;
-  k.p_first = k.shift + quotient(r0, p.by_group);
-  k.p_last = k.shift + quotient(r_last, p.by_group);
-  k.hi = min(w.kv_len, k.p_last + 1);
-  if (p.kv_len) k.hi = min(k.hi, p.table_keys);
-  k.lo = max(0, k.p_first - p.window + 1);
-  k.sinks = min(p.sinks, k.hi);
-  k.sink_end = (max(k.sinks, 0) + G - 1) & ~(G - 1);
-  k.skip = max(0, (k.lo & ~31) - k.sink_end);
-  k.end = max(k.hi - k.skip, min(k.hi, k.sink_end));  // (the table may end before the window)
-  k.start = 0;
-  if (w.splits > 1) {
-    const int64_t from = (int64_t)w.split * w.part_keys;
-    k.start = (int)min<int64_t>(from, MAX_KEYS);
-    k.end = (int)min<int64_t>(from + w.part_keys, k.end);
-  }
-  return k;
 }
 
 // ------------------------------------------- shared keys, then own keys

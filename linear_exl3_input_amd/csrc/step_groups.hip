@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void groups_kernel(GroupsParams p) {
   for (int s = s0 + lane; s < s1; s += 64) {
     const int n = p.seq_row[s + 1] - p.seq_row[s];
     if (n > 0) {
-      before = min(before, max(p.kv_len[s], 0) - n);
+      before = min(before, counted_keys(p.kv_len[s]) - n);
       lead = min(lead, s);
       ++live;
     }
