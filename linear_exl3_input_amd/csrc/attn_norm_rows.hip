@@ -196,7 +196,7 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormRowsParams np) {
       eight_floats<BF16>(own[i], f);
       if (p.interleaved) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = f[j ^ 1];
+        for (int j = 0; j < 8; ++j) g[j] = turns ? f[j ^ 1] : 0.f;  // (B is 0 there, but an infinity times 0 is NaN)
       } else {
         eight_floats<BF16>(other[i], g);
       }

@@ -129,6 +129,28 @@ def test_norm_of_zeros_large_values_and_what_is_not_finite():
         assert torch.isnan(got[5, 2, i]) if i in bad else got[5, 2, i] == 0
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 16), (64, 64), (128, 32), (128, 128), (256, 64), (256, 240)])
+@pytest.mark.parametrize("tokens,heads", [(3, 2), (3000, 6)])  # one and two rows a lane
+def test_infinities_stay_with_their_value_and_its_pair(tokens, heads, d, rot, interleaved):
+    """The mean is infinite: 0 for the finite values, NaN for an infinite one and, where it turns, for its pair."""
+    r = ex.Rope.make(rot, 1e4, 8, interleaved=interleaved)
+    pos = torch.arange(tokens, dtype=torch.int32) % 7 + 1
+    x = normal((tokens, heads, d), 5, BF16)
+    norm = ex.HeadNorm((normal((d,), 6, torch.float32) + 3).cuda(), eps=1e-6)
+    half = rot // 2
+    pair = lambda i: i if i >= rot else i ^ 1 if interleaved else (i + half) % rot  # noqa: E731
+    bad = torch.zeros(x.shape, dtype=torch.bool)
+    for t, h, places in ((0, 0, (d - 1,)), (1, 1, (rot // 2,)), (2, 0, (0, d - 2, rot - 1)), (tokens - 1, heads - 1, (rot % d, d - 4))):
+        for n, i in enumerate(places):
+            x[t, h, i] = float("-inf") if n else float("inf")
+            bad[t, h, i] = bad[t, h, pair(i)] = True
+    infinite = torch.isinf(x).any(-1, keepdim=True)
+    got = ex.rope(r, pos.cuda(), x.cuda(), norm=norm).cpu()
+    assert torch.equal(torch.isnan(got), bad)
+    assert not got[infinite & ~bad].any() and not torch.isinf(got).any()
+
+
 def test_weights_one_plus_and_copies():
     r = ex.Rope.make(128, 1e4, 40)
     pos, x = whole(40, 40, 1), normal((40, 4, 128), 2, F16)
