@@ -214,7 +214,9 @@ size_t exl3_workspace_bytes(const exl3_weight *w, int32_t M);
  *             Its first EXL3_WORKSPACE_COUNTER_BYTES are arrival counters that
  *             must be zero on entry (allocate the workspace zeroed once) and
  *             are zero again when the call's kernels end; the rest may hold
- *             anything.  A workspace serves one call at a time.
+ *             anything.  A workspace serves one call at a time: on one stream
+ *             calls follow one another, also those of several host threads
+ *             (no launch of one comes between the launches of another).
  * In slab mode the workgroups of a tile that finish first store their
  * partial and count their arrival; the last to arrive sums the partials in
  * the plan's order and writes y (TensorFold PR, "Arithmetic": the last part

@@ -221,7 +221,9 @@ class Exl3Weight:
 # Process-wide workspaces (the cuda-exl3 page, "VRAM": the activation and
 # split-k workspaces are process-wide, not per layer), one per (device,
 # stream): calls on one stream run one after another, so they may share one
-# workspace, while calls on two streams may overlap and get one each.  The
+# workspace, while calls on two streams may overlap and get one each.  (Calls
+# of several host threads on one stream, too: the library makes a call's
+# launches on a workspace without others' between them.)  The
 # first COUNTER_BYTES of a workspace are the arrival counters that every call
 # expects zero and leaves zero.  A workspace is never freed once handed out
 # (a captured graph keeps its address): a larger one replaces it for later

@@ -385,7 +385,9 @@ exl3_status run_attention(AttnParams &p, int32_t head_dim, int32_t q_heads, void
                           Launch launch) {
   AttnPlan pl;
   const exl3_status st = plan_attention(p.batch, p.tokens, q_heads, p.heads_kv, head_dim, &pl);
-  return st != EXL3_OK ? st : run_planned(p, pl, workspace, workspace_bytes, launch);
+  if (st != EXL3_OK) return st;
+  const WorkspaceTurn turn(pl.workspace > 0 ? workspace : nullptr);
+  return run_planned(p, pl, workspace, workspace_bytes, launch);
 }
 
 }  // namespace exl3

@@ -709,6 +709,7 @@ exl3_status exl3_linear_ex(const exl3_weight *w, const uint16_t *x_rot, int32_t 
   uint16_t *dense =
       pl.decoder == EXL3_DECODER_DENSE ? reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + pl.dense_off)
                                        : nullptr;
+  const exl3::WorkspaceTurn turn(pl.workspace > 0 ? workspace : nullptr);
   return run_linear(w, x_rot, M, y, y_dtype, counters, slabs, dense, pl, (hipStream_t)stream, true);
 }
 
@@ -890,6 +891,7 @@ exl3_status exl3_forward(const exl3_weight *w, const void *x, int32_t x_dtype, i
       pl.decoder == EXL3_DECODER_DENSE ? reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + pl.dense_off)
                                        : nullptr;
   const hipStream_t s = (hipStream_t)stream;
+  const exl3::WorkspaceTurn turn(need > 0 ? workspace : nullptr);
   if (rotation_in_gemm(w, pl, M))
     return run_linear(w, nullptr, M, y, y_dtype, counters, slabs, dense, pl, s, true, nullptr, 0, 0, x,
                       x_dtype == EXL3_BF16);
@@ -988,11 +990,14 @@ exl3_status exl3_tune(const exl3_weight *ws, int32_t n_w, const uint16_t *x_rot,
       uint16_t *dense = pl.decoder == EXL3_DECODER_DENSE
                             ? reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + pl.dense_off)
                             : nullptr;
+      auto run = [&](const exl3_weight *copy) {
+        const exl3::WorkspaceTurn turn(pl.workspace > 0 ? workspace : nullptr);
+        return run_linear(copy, x_rot, M, y, y_dtype, counters, slabs, dense, pl, s, true);
+      };
       auto timed = [&](int n, float *ms) -> exl3_status {
         if ((e = hipEventRecord(e0, s)) != hipSuccess) return launch_error(e, "event record");
         exl3_status r = EXL3_OK;
-        for (int k = 0; k < n && r == EXL3_OK; ++k)
-          r = run_linear(&ws[(k + 1) % n_w], x_rot, M, y, y_dtype, counters, slabs, dense, pl, s, true);
+        for (int k = 0; k < n && r == EXL3_OK; ++k) r = run(&ws[(k + 1) % n_w]);
         if (r != EXL3_OK) return r;
         if ((e = hipEventRecord(e1, s)) != hipSuccess || (e = hipEventSynchronize(e1)) != hipSuccess)
           return launch_error(e, "event wait");
@@ -1001,7 +1006,7 @@ exl3_status exl3_tune(const exl3_weight *ws, int32_t n_w, const uint16_t *x_rot,
       };
       float ms1 = 0.f, ms = 0.f;
       // one untimed call, one timed call to size the batch, then the batch
-      if ((st = run_linear(w, x_rot, M, y, y_dtype, counters, slabs, dense, pl, s, true)) != EXL3_OK) break;
+      if ((st = run(w)) != EXL3_OK) break;
       if ((st = timed(1, &ms1)) != EXL3_OK) break;
       const int n = std::min(1000, std::max(reps, (int)(2.0f / std::max(ms1, 1e-4f)) + 1));
       if ((st = timed(n, &ms)) != EXL3_OK) break;
@@ -1234,6 +1239,7 @@ exl3_status exl3_moe_linear_ex(const exl3_weight *w, int32_t E, const uint16_t *
   uint32_t *counters = static_cast<uint32_t *>(workspace);
   float *slabs = pl.workspace > 0 ? reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.slab_off) : nullptr;
   const int64_t expert_words = (int64_t)w->K / 16 * (w->N / 16) * 16 * w->bits;
+  const exl3::WorkspaceTurn turn(pl.workspace > 0 ? workspace : nullptr);
   return run_linear(w, x_rot, rows, y, y_dtype, counters, slabs, nullptr, pl, (hipStream_t)stream, true, block_expert,
                     expert_words, E);
 }
@@ -1522,6 +1528,7 @@ exl3_status linear_in_scratch(const exl3_weight *w, const uint16_t *x_rot, int32
   uint16_t *dense = pl.decoder == EXL3_DECODER_DENSE
                         ? reinterpret_cast<uint16_t *>(static_cast<char *>(scratch) + pl.dense_off)
                         : nullptr;
+  const exl3::WorkspaceTurn turn(pl.workspace > 0 ? scratch : nullptr);
   return run_linear(w, x_rot, M, y, y_dtype, counters, slabs, dense, pl, (hipStream_t)stream, true);
 }
 
@@ -1538,5 +1545,17 @@ exl3_status host_fail(exl3_status s, const char *fmt, ...) {
 void host_clear_error() { clear_error(); }
 
 int host_cus() { return device_cus_or_default(); }
+
+// Workspaces that share a mutex wait for each other a little; no call holds two.
+static std::mutex g_turns[64];
+
+WorkspaceTurn::WorkspaceTurn(const void *workspace)
+    : turn_(workspace == nullptr ? -1 : (int)((reinterpret_cast<uintptr_t>(workspace) >> 4) * 0x9E3779B97F4A7C15ull >> 58)) {
+  if (turn_ >= 0) g_turns[turn_].lock();
+}
+
+WorkspaceTurn::~WorkspaceTurn() {
+  if (turn_ >= 0) g_turns[turn_].unlock();
+}
 
 }  // namespace exl3

@@ -102,6 +102,7 @@ exl3_status run_sinks(AttnParams &p, int32_t head_dim, bool bf16, int32_t bits, 
       plan_split(p.batch, p.tokens, q_heads, p.heads_kv, head_dim,
                  plan_columns(p.batch, p.tokens, q_heads, p.heads_kv, head_dim), &pl, rounds);
   if (st != EXL3_OK) return st;
+  const WorkspaceTurn turn(pl.workspace > 0 ? workspace : nullptr);
   return run_planned(p, pl, workspace, workspace_bytes,
                      [&](int columns) { return launch_attn_sinks(head_dim, bf16, bits, p, columns, s); });
 }
@@ -436,6 +437,7 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
   g.group = p.group;
   g.tile_rows = tile_rows(pl.own.columns);
   p.group_items = take(2 * (int64_t)groups);
+  const WorkspaceTurn turn(workspace);
   if (batch >= FEW_SEQUENCES && (st = launched(launch_groups(g, s), "groups launch")) != EXL3_OK) return st;
   p.state = reinterpret_cast<float *>(ws + pl.state);
   PrefixParams shared;
