@@ -97,8 +97,12 @@ exl3_status exl3_prompt_attention_sinks(const exl3_rows *q, const exl3_rows *k, 
  * group's sequences are read once for all of them; the result is
  * exl3_paged_attention's but for the order of sums.  Calls that gain nothing by
  * it, by their sizes (few sequences, a narrow page table or more than 512 rows of a
- * sequence on each key/value head, on average), are one launch of
- * that, others two, or four of 256 sequences and more.  An offset in group_cu
+ * sequence on each key/value head, on average), and those that would leave more
+ * than 1 GiB between the passes are one launch of that, others two, or four of
+ * 256 sequences and more.  The sizes are those that the host has: a page table
+ * counts as full to its width.  One as wide as the longest sequence lets short
+ * calls be one launch (4 sequences of 1100 keys, 8 heads of 128: 11 us; with a
+ * table for 16384 keys or more they take the two passes, 18).  An offset in group_cu
  * counts as at least those before it and at most batch. */
 exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, const exl3_rows *out,
                                   const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
@@ -107,7 +111,9 @@ exl3_status exl3_prefix_attention(const exl3_kv_cache *c, const exl3_rows *q, co
                                   void *workspace, size_t workspace_bytes, void *stream);
 
 /* Workspace of exl3_prefix_attention, with counters at its start like that of
- * the other attention calls, which may be the same. */
+ * the other attention calls, which may be the same.  It does not depend on the
+ * page table, so that what is reserved before a capture serves every table; it is
+ * at most 1 GiB more than exl3_attention_workspace_bytes's and some arrays. */
 size_t exl3_prefix_attention_workspace_bytes(int32_t batch, int32_t tokens, int32_t groups, int32_t q_heads,
                                              int32_t kv_heads, int32_t head_dim);
 

@@ -634,7 +634,9 @@ def prefix_attention(cache: KvCache, q: torch.Tensor, cu_q: torch.Tensor, kv_len
     Group g is the sequences group_cu[g]..group_cu[g+1]-1 (int32 [groups+1]); their rows of the page table have the same
     pages for their first prefix_len[g] keys (int32 [groups]; rows of sequences without new tokens may hold anything).
     Sequences of no group share nothing.  The rest is paged_attention's, and so is the result but for the order of
-    sums."""
+    sums.  Whether sharing is worth its passes is decided by the sizes, a page table counting as full to its width: one
+    much wider than the sequences makes short calls slower (18 us instead of 11).  The workspace (up to 1 GiB more than
+    paged_attention's) is kept for the stream."""
     if _current_device() != cache.device.index:
         with torch.cuda.device(cache.device):
             return prefix_attention(cache, q, cu_q, kv_len, page_table, group_cu, prefix_len, scale, out)

@@ -131,10 +131,20 @@ constexpr double SHARED_BYTES_MIN = 192e6;
 
 // And so is a call whose sequences fill the tile kernel's tiles by themselves, for
 // what every tile leaves costs more than the keys: by the average rows of a
-// sequence on a key/value head, over 8192 shared keys, shared / plain, 256 rows
-// 180 / 212 us, 512 275 / 270 (64 sequences 828 / 925), 1024 520 / 434 (24/4 heads of
-// 256, 1536 rows 780 / 838), 2048 850 / 838.  It also bounds the workspace.
+// sequence on a key/value head, over 8192 shared and 150 own keys, 32/8 heads of 128,
+// 8 bits, shared / plain, 16 sequences of 256 rows 215 / 252 us, 512 361 / 380, 1024
+// 666 / 656, 2048 1275 / 1227; 64 sequences of 256 rows 671 / 657, 512 1319 / 1252, 1024
+// 2598 / 2472; 24/4 heads of 256, 16 sequences of 1536 rows 1396 / 1393.
 constexpr int64_t SHARED_ROWS_MAX = 512;
+
+// And so is a call whose state would be larger than this: it grows with the query
+// rows (528 bytes each with heads of 128) where the plain call's parts do not.
+// What it costs: with 32 heads of 128 a call reaches it at 60000 tokens, where
+// sharing 8192 keys still gains a quarter if a sequence has 64 rows on a key/value
+// head (2048 sequences of 16 tokens, 593 MB, 6631 / 8890 us), and nothing if it has
+// 128 and more (512 of 32 tokens, 312 MB, 2575 / 2461; 2048 of 64 tokens, 64 heads,
+// 4.5 GB, 40548 / 39605).
+constexpr size_t STATE_MAX = (size_t)1 << 30;
 
 bool worth_sharing(const exl3_kv_cache *c, int32_t page_table_width, int32_t batch, int32_t groups) {
   const double row = c->head_dim * c->bits / 8.0 + (c->bits < 16 ? c->head_dim / 32.0 : 0.0);
@@ -173,15 +183,15 @@ exl3_status plan_prefix(int32_t batch, int32_t tokens, int32_t groups, int32_t q
   pl->shared.part_min = 256;
   pl->rows_log2 = __builtin_ctz((unsigned)tile_rows(pl->shared.columns));
   const int64_t items = ((int64_t)tokens * (q_heads / kv_heads) >> pl->rows_log2) + groups + pl->shared.target;
-  if (items * kv_heads > MAX_GRID)
-    return host_fail(EXL3_ERR_UNSUPPORTED, "%d tokens x %d heads: more tiles than a launch holds", tokens, q_heads);
+  const int64_t state_rows = items * kv_heads << pl->rows_log2;
+  const size_t state = sizeof(float) * (size_t)state_rows * (STATE_PAD + head_dim);
+  pl->shares = state <= STATE_MAX;  // (a launch holds the tiles of far larger ones)
+  if (!pl->shares) return EXL3_OK;
   pl->items = (int32_t)items;
   auto whole = [](size_t n) { return (n + 255) & ~(size_t)255; };
   pl->ints = whole(std::max(pl->own.workspace, (size_t)EXL3_WORKSPACE_COUNTER_BYTES));
   pl->state = pl->ints + whole(sizeof(int32_t) * (4 * (size_t)batch + 2 + 6 * (size_t)groups + 2));
-  pl->workspace = std::max(
-      pl->workspace,
-      pl->state + sizeof(float) * ((size_t)pl->items * kv_heads << pl->rows_log2) * (STATE_PAD + head_dim));
+  pl->workspace = std::max(pl->workspace, pl->state + state);
   return EXL3_OK;
 }
 

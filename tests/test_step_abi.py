@@ -243,3 +243,16 @@ def test_prefix_workspace():
     for args in ((-1, 1, 0, 4, 4, 128), (1, 1, 2, 4, 4, 128), (1, 1, -1, 4, 4, 128), (1, 1, 1, 5, 4, 128), (1, 1, 1, 4, 4, 100)):
         with pytest.raises(ex.Exl3Error):
             ex.prefix_attention_workspace_bytes(*args)
+
+
+def test_the_prefix_workspace_is_bounded():
+    """At most 1 GiB more than the groups' arrays (24 bytes a sequence and a group) and parts of own keys, whatever the sizes."""
+    for d in (64, 128, 256):
+        for hq, hkv in ((1, 1), (32, 8), (64, 8), (24, 4), (1024, 1024), (1024, 8)):
+            for batch in (1, 16, 256, 2048, 16384, 65536):
+                for each in (1, 8, 64, 512):
+                    if batch * each <= 1 << 20:
+                        for groups in {0, 1, batch // 8, batch}:
+                            need = ex.prefix_attention_workspace_bytes(batch, batch * each, groups, hq, hkv, d)
+                            plain = ex.attention_workspace_bytes(batch, batch * each, hq, hkv, d)
+                            assert need <= (1 << 30) + (1 << 20) + plain + 48 * batch + 16384 * 16 * (d + 2) * 4, (batch, each, groups, hq, hkv, d)

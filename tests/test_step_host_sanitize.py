@@ -57,6 +57,17 @@ def test_the_passes_of_a_call_with_shared_prefixes(driver, sizes, want):
     assert driver(*sizes).split() == want.split()
 
 
+@pytest.mark.parametrize("sizes,want", [
+    ((2048, 32768, 8, 32, 8, 128, 8, 600), "shared tile small whole"),   # 0.6 GB of state
+    ((16384, 16384, 16, 32, 8, 128, 8, 300), "shared tile small whole"),
+    ((2048, 65536, 8, 32, 8, 128, 8, 600), "plain none none whole"),     # 1.1 GB
+    ((2048, 131072, 1, 64, 8, 128, 8, 600), "plain none none whole"),    # 4.5
+    ((16384, 1048576, 1, 64, 8, 128, 8, 600), "plain none none whole"),  # 35
+    ((65536, 65536, 1, 64, 8, 128, 8, 300), "plain none none whole")])   # 2.3
+def test_calls_whose_state_would_be_too_large_are_plain(driver, sizes, want):
+    assert driver(*sizes).split() == want.split()
+
+
 @pytest.mark.parametrize("bits,d,hkv,page", [(16, 64, 1, 16), (8, 128, 2, 64), (4, 256, 8, 256)])
 def test_the_wide_tables_of_the_gpu_tests_make_a_call_share(driver, bits, d, hkv, page):
     """test_gpu_step_prefix.widened's number of columns, for two sequences and one group."""
