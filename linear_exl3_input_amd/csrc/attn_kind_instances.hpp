@@ -9,6 +9,10 @@ namespace {
 
 using Params = std::conditional_t<EXL3_KIND == ATTN_PREFIX, PrefixParams, AttnParams>;
 
+// Two column tiles of 256-value heads do not fit the registers, and own keys
+// take one (plan_prefix).
+constexpr bool TWO_COLUMNS = EXL3_HEAD_DIM < 256 && EXL3_KIND != ATTN_OWN;
+
 // As many workgroups as a plain launch has.
 template <bool BF16, int BITS>
 hipError_t launch_columns(const Params &p, int columns, hipStream_t s) {
@@ -18,11 +22,10 @@ hipError_t launch_columns(const Params &p, int columns, hipStream_t s) {
     hipLaunchKernelGGL((attn_tile_kernel<BF16, EXL3_HEAD_DIM, BITS, EXL3_KIND, Params>), grid, block, 0, s, p);
   else if (columns == 1)
     hipLaunchKernelGGL((attn_small_kernel<BF16, EXL3_HEAD_DIM, BITS, 1, EXL3_KIND, Params>), grid, block, 0, s, p);
-#if EXL3_HEAD_DIM < 256  // two column tiles of 256-value heads do not fit the registers
-  else if (columns == 2)
+  else if constexpr (TWO_COLUMNS) {
+    if (columns != 2) return hipErrorInvalidValue;
     hipLaunchKernelGGL((attn_small_kernel<BF16, EXL3_HEAD_DIM, BITS, 2, EXL3_KIND, Params>), grid, block, 0, s, p);
-#endif
-  else
+  } else
     return hipErrorInvalidValue;
   return hipGetLastError();
 }
