@@ -115,7 +115,7 @@ exl3_status exl3_cache_read(const exl3_kv_cache *c, const int32_t *slots, int32_
  * j % page_size of page page_table[s][j / page_size] (int32, row stride
  * page_table_stride, width page_table_width); a page outside 0..pages-1, or
  * past the width, is a hole whose keys nobody sees.  A length in kv_len counts
- * as 0 to 2^31 - 2^16.  Query head h reads the cache's head
+ * as 0 to 2^31 - 2^21.  Query head h reads the cache's head
  * h / (q.heads / heads).  Rows that see no key are zero.  An offset in cu_q
  * counts as at least those before it and at most tokens; rows that then belong
  * to no sequence are not written.

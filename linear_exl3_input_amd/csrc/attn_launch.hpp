@@ -80,6 +80,7 @@ struct ReadParams {
 // Keys of a sequence that the kernels address; positions past them, and steps
 // that run a little past a sequence's end, still fit 32 bits.
 constexpr int32_t MAX_KEYS = 0x7FFF0000;
+constexpr int32_t MAX_LENGTH = 0x7FE00000;  // and what a length in device memory counts as at most (counted_keys)
 
 // Attention over a paged cache (cache.k set) or packed rows (k.data set).
 struct AttnParams {

@@ -44,9 +44,11 @@ struct Work {
 };
 
 // A sequence's keys by its length in device memory, which nothing has checked.
-// Past MAX_KEYS a window's first key, the steps' and the look-ups' ahead of them
-// would pass 2^31, and a page be looked up before the table.
-EXL3_BOTH int counted_keys(int kv_len) { return least(most(0, kv_len), MAX_KEYS); }
+// Near 2^31 a window's first key, and the steps and look-ups ahead of it, would
+// pass 2^31, and a page be looked up before the table.  MAX_LENGTH leaves room for
+// where a part of a window and first tokens can start: up to 2^20 places past the
+// window, and 127 for each of 4096 parts.
+EXL3_BOTH int counted_keys(int kv_len) { return least(most(0, kv_len), MAX_LENGTH); }
 
 // The keys that a workgroup reads, [lo, hi), of those the tile's rows r0 ..
 // r_last see, and the multiple of 32 where it starts.
@@ -99,7 +101,7 @@ EXL3_BOTH KeyRange sink_range(const AttnParams &p, const Work &w, int r0, int r_
   k.start = 0;
   if (w.splits > 1) {
     const int64_t from = (int64_t)w.split * w.part_keys;
-    k.start = (int)least<int64_t>(from, MAX_KEYS - k.skip);  // (there it is past the end)
+    k.start = (int)least<int64_t>(from, MAX_KEYS);
     k.end = (int)least<int64_t>(from + w.part_keys, k.end);
   }
   return k;

@@ -36,7 +36,7 @@ static void sinks(const AttnParams &p, const Work &w, int r0, int r_last) {
 }
 
 int main() {
-  const int kvs[] = {(int)0x80000000, -5, 0, 1, 100, 5000, 1 << 20, 1 << 30, MAX_KEYS - 1, MAX_KEYS, MAX_KEYS + 1, 0x7FFFFF00, 0x7FFFFFFE, 0x7FFFFFFF};
+  const int kvs[] = {(int)0x80000000, -5, 0, 1, 100, 5000, 1 << 20, 1 << 30, MAX_LENGTH - 1, MAX_LENGTH, MAX_LENGTH + 1, MAX_KEYS, 0x7FFFFF00, 0x7FFFFFFE, 0x7FFFFFFF};
   const int rows[] = {1, 2, 90, 1 << 20};
   const int windows[] = {0, 1, 100, 4096, 1 << 29, 1 << 30};
   const int firsts[] = {0, 1, 4, 130, 1 << 20};

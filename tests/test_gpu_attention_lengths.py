@@ -14,7 +14,7 @@ from test_gpu_step_sinks import BF16, Paged, same_bits
 pytestmark = pytest.mark.gpu
 
 FAR = 2 ** 30 + 2 ** 20  # a window of 2^30 does not reach the table
-LENGTHS = [2 ** 31 - 2 ** 16 - 1, 2 ** 31 - 2 ** 16, 2 ** 31 - 2 ** 16 + 1, 2 ** 31 - 300, 2 ** 31 - 1]
+LENGTHS = [2 ** 31 - 2 ** 21 - 1, 2 ** 31 - 2 ** 21, 2 ** 31 - 2 ** 21 + 1, 2 ** 31 - 300, 2 ** 31 - 1]
 
 
 def ints(*x):
