@@ -159,6 +159,20 @@ def test_groups_of_every_size_by_either_form(batch):
     pairs.check()
 
 
+@pytest.mark.parametrize("bits,dtype,d", base.FORMATS)
+@pytest.mark.parametrize("n", [1, 3])
+def test_the_smallest_groups(n, bits, dtype, d):
+    """Two sequences in one group, with one beside them, with sequences of no group (more sequences than groups: the
+    shared passes take them; as many of both are one plain launch)."""
+    for groups in ([(64, [(n, n), (n, n + 5)])], [(96, [(n, n + 40), (1, 2)]), (32, [(n, n + 7)])],
+                   [(32, [(0, 4), (n, n + 9), (2, 3)]), (48, [])]):
+        x = Shared(groups, 4, 2, d, dtype, bits, 16, seed=32)
+        assert len(x.kv_lens) > len(x.groups)
+        want = x.check()
+        ref.check(x.run(group_cu=[0, 2], prefix=[x.shared[0]]), *want, "the first two")
+        ref.check(x.run(group_cu=[1, len(x.kv_lens)], prefix=[0]), *want, "a group that shares nothing")
+
+
 @pytest.mark.parametrize("n", [128, 129])
 def test_chunks_up_to_and_past_what_is_shared(n):
     """512 rows of a sequence on each key/value head are the most that the shared passes take."""
