@@ -30,7 +30,8 @@ typedef struct exl3_rotary_axes {
 /* Norms of each query and key head, before the rotation:
  *   n = x / sqrt(mean(x^2) + eps) * w
  * over the head's values.  w fp32: head_dim weights for all heads, or one such
- * row for each (q_rows, k_rows: 1 or the number of heads). */
+ * row for each (q_rows, k_rows: 1 or the number of heads).  x * w stays within
+ * fp32's range (it is taken before the division). */
 typedef struct exl3_head_norm {
   const float *q, *k;
   int32_t q_rows, k_rows;

@@ -359,9 +359,9 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int item, int lan
 //   o = (o1 2^(m1-m) + o2 2^(m2-m)) / (l1 2^(m1-m) + l2 2^(m2-m)).
 // Every part of a group's tile leaves its rows (m, l, o; nothing is joined
 // there), and the first part of a row's own keys adds them up in a fixed order.
-// What bounds the shared keys is vector work beside the products at 8 bits (matrix
-// units busy 20% of the cycles, vector units 37%) and a start and end of 14 us;
-// the own keys the latency of the longest sequence.  Measured: 64 sequences
+// What bounds the shared keys is latency that two waves a SIMD do not hide (at 8
+// bits matrix units busy 20% of the cycles, vector units 36%, HBM at 2 TB/s), and a
+// start and end of 14 us; the own keys the latency of the longest sequence.  Measured: 64 sequences
 // over 24000 shared and up to 1500 own keys, 32/8 heads of 128, 8 bits: 49 us
 // for the shared keys in 32 parts of 768, 39 for the own, of which 8 are the 34 MB
 // that the parts left.  (Joined by the last part to arrive, as split tiles are

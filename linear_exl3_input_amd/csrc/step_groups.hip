@@ -7,7 +7,8 @@ namespace exl3 {
 // Running maxima of the offsets, and the tiles of own keys' rows before each
 // sequence, by one workgroup, then a wave to a group: two launches of 5 us, whose
 // chains of loads and barriers are what bounds them.  (A wave to a group in the
-// first one's workgroup: 500 groups of two 87 us, 2000 361.)
+// first one's workgroup: 500 groups of two 87 us, 2000 361.  4000 sequences in 4
+// groups: 9 and 16 us.)
 __global__ __launch_bounds__(1024) void rising_kernel(GroupsParams p) {
   constexpr int N = 1024;
   __shared__ int s_top[3][N / 64];

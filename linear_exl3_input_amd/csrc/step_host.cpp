@@ -125,8 +125,11 @@ struct PrefixPlan {
 // and 8192 (75, 270) 22 / 27 and 27 / 46, 64 of 512 and 2048 (111, 315) 29 / 27 and
 // 32 / 47; 8 tokens each, 16 of 8192 (270) 53 / 52.  24/4 heads of 256 need more, at
 // 4 bits 24 sequences of 8192 (213) 55 / 44, 32 (287) 57 / 50 and 64 (583) 66 / 87;
-// 32/8 heads of 256 do not, 16 of 8192 (278) 34 / 50.  The host knows the page
-// table's width alone, so that counts as every sequence's keys.
+// 32/8 heads of 256 do not, 16 of 8192 (278) 34 / 50.  One number for all of them:
+// it shares the 24 and 32 sequences of those wide heads, 11 and 7 us too slow, and
+// leaves the 16 of 2048 keys plain, where later measurements found no difference
+// (26 / 26; 64 of 512 25 / 25).  The host knows the page table's width alone, so
+// that counts as every sequence's keys.
 constexpr double SHARED_BYTES_MIN = 192e6;
 
 // And so is a call whose sequences fill the tile kernel's tiles by themselves, for
